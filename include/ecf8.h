@@ -92,6 +92,9 @@ extern "C" {
 #define ECF8_STATUS_BAD_CODE 2       /* bits that match no code */
 #define ECF8_STATUS_BAD_OFFSETS 4    /* group offsets not monotone or past n */
 #define ECF8_STATUS_BOUNDS 8         /* checked builds only: an index failed its bounds check */
+/* bits OR-ed into *d_status by the linear and gradient calls */
+#define ECF8_STATUS_BAD_REQUEST 16 /* request offsets not monotone in [0, rows], or an adapter id past the last */
+#define ECF8_STATUS_NONFINITE 32   /* the norm of a gradient set is not finite */
 
 /* A canonical Huffman code over the 16 exponent values. */
 typedef struct ecf8_codebook {
@@ -324,6 +327,129 @@ int ecf8_pipeline_release(ecf8_pipeline* p, int layer, cudaStream_t compute);
 /* Frees the pipeline's events and host state (work already enqueued still
  * runs to completion). */
 void ecf8_pipeline_destroy(ecf8_pipeline* p);
+
+/* ---------------------------------------------------------------------------
+ * Linear layers over decoded weights, with low-rank adapters.
+ *
+ * What a decoded tensor is read by: y = s * (x W^T), W the n_out x k_in E4M3
+ * bytes a decode wrote, s one scale for the tensor or one per output row.
+ * Beside that shared projection each request may add an adapter of its own,
+ * the form in which one compressed base model serves or trains many
+ * fine-tunings at once:
+ *     y[t] = s * (W x[t]) + alpha[a] * B[a] (A[a] x[t]),   a = adapter of row t.
+ * Request i is the rows d_offsets[i] .. d_offsets[i+1]-1 and uses adapter
+ * d_ids[i]; a negative id means none, and so do rows outside every request
+ * (before d_offsets[0], or from d_offsets[count] on, as in a padded batch).
+ * An id may occur in any number of requests; requests may be empty.  Both
+ * arrays are read on the device, so a captured call follows them.
+ *
+ * x, y, A, B and the gradients are all of one type, BF16 or FP16 (d_w is
+ * always E4M3, scales and alpha float32).  Products are summed in float32 and
+ * rounded once, when a result is written.  Rows of x, y and W may be strided;
+ * every pointer needs the alignment of its type, and sizes may be odd.
+ * (BF16/FP16 pointers and row strides of 16 bytes, and d_w and w_stride of 16,
+ * take the tensor-core path when k_in and n_out are multiples of 16.)
+ * Outputs must not overlap inputs.  E4M3 NaN bytes count as NaN.  A row's
+ * result depends on its own row of x and its own adapter only: an adapter that
+ * holds infinities or NaN leaves the other requests' rows as they would be.
+ *
+ * A request table that is not monotone in [0, rows] or names an adapter past
+ * the last ORs ECF8_STATUS_BAD_REQUEST into *d_status; the rows it concerns
+ * then get unspecified values, and nothing is accessed out of bounds. */
+#define ECF8_DTYPE_BF16 0
+#define ECF8_DTYPE_FP16 1
+#define ECF8_DTYPE_FP32 2 /* gradient sets only */
+
+/* Largest rank of an adapter; adapters of lower rank are padded with zeros. */
+#define ECF8_RANK_MAX 128
+
+typedef struct ecf8_linear {
+  const uint8_t* d_w;   /* n_out rows of k_in E4M3 bytes, w_stride bytes apart */
+  uint64_t n_out, k_in;
+  uint64_t w_stride;    /* at least k_in */
+  const float* d_scale; /* n_scale float32; NULL with n_scale = 0: 1.0 */
+  uint64_t n_scale;     /* 0, 1 or n_out */
+  const void* d_a;      /* n_adapters x rank x k_in */
+  const void* d_b;      /* n_adapters x n_out x rank */
+  const float* d_alpha; /* n_adapters */
+  uint32_t n_adapters;  /* 0: no adapters, d_a, d_b and d_alpha are not read */
+  uint32_t rank;        /* 1..ECF8_RANK_MAX */
+  int32_t dtype;        /* ECF8_DTYPE_BF16 or ECF8_DTYPE_FP16 */
+} ecf8_linear;
+
+typedef struct ecf8_requests {
+  const int32_t* d_offsets; /* device, count + 1 */
+  const int32_t* d_ids;     /* device, count */
+  uint32_t count;
+} ecf8_requests;
+
+/* Bytes of device workspace a forward or backward call of this many rows
+ * needs (0 without adapters). */
+size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows);
+
+/* y = s * (x W^T) + the adapters' part, for `rows` rows.  requests may be NULL
+ * (no row has an adapter).  d_u (nullable; float32, rows x rank) keeps A[a] x[t] for
+ * a backward pass, 0 for rows without an adapter; NULL keeps it in the
+ * workspace.  d_workspace (16-byte aligned) belongs to the call until it ends
+ * on the stream.  Strides count elements.  Asynchronous on stream s; errors
+ * are returned before anything is enqueued: ECF8_ERR_ARG (null or bad sizes),
+ * ECF8_ERR_ALIGN, ECF8_ERR_WORKSPACE, ECF8_ERR_CUDA. */
+int ecf8_linear_forward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,
+                        void* d_y, uint64_t y_stride, uint64_t rows, float* d_u, void* d_workspace,
+                        size_t workspace_bytes, int32_t* d_status, cudaStream_t s);
+
+/* Gradients of ecf8_linear_forward for a given dy (W and the scales are
+ * frozen).  Each output may be NULL to leave it out:
+ *     dx[t]    = W^T (s * dy[t]) + alpha[a] * A[a]^T (B[a]^T dy[t])
+ *     da[a]    = alpha[a] * sum over a's rows of (B[a]^T dy[t]) x[t]^T
+ *     db[a]    = alpha[a] * sum over a's rows of dy[t] u[t]^T
+ * da and db have the layout of A and B and are overwritten, with zeros for
+ * adapters that no row uses; an adapter's rows are summed over all its
+ * requests, in an order that does not vary.  d_u is the forward call's (read
+ * for db only), d_x is read for da only.  With one scale per output row the
+ * tensor-core path rounds s * W to the activation type before the product. */
+int ecf8_linear_backward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,
+                         const void* d_dy, uint64_t dy_stride, const float* d_u, void* d_dx, uint64_t dx_stride,
+                         void* d_da, void* d_db, uint64_t rows, void* d_workspace, size_t workspace_bytes,
+                         int32_t* d_status, cudaStream_t s);
+
+/* ---------------------------------------------------------------------------
+ * The global norm of a set of gradient tensors, and clipping by it (the step
+ * between a backward pass over many adapters and the optimiser).  Like a
+ * batched decode, one call takes all tensors; their descriptors are laid out
+ * once, on the host, into a table that the caller copies to the device. */
+typedef struct ecf8_grad {
+  const void* d_in; /* device, aligned to its type */
+  void* d_out;      /* device: d_in itself, or a buffer that overlaps no tensor of the set; NULL: norm only */
+  uint64_t n;       /* values; 0 is allowed */
+  int32_t dtype;    /* ECF8_DTYPE_* */
+} ecf8_grad;
+
+/* Bytes of the table of count tensors. */
+size_t ecf8_grad_table_bytes(int count);
+
+/* Fill h_table (host, ecf8_grad_table_bytes(count) bytes) for these tensors.
+ * The set is fixed by it: pointers, sizes and types.  ECF8_ERR_ARG,
+ * ECF8_ERR_ALIGN. */
+int ecf8_grad_build_table(const ecf8_grad* grads, int count, void* h_table);
+
+/* Bytes of device workspace a norm or clip call needs. */
+size_t ecf8_grad_workspace_size(void);
+
+/* *d_norm (device float32) = the L2 norm of all values of the set, squares
+ * summed in float64 in an order that does not vary.  d_table is the device
+ * copy of h_table, which the call also reads on the host.  Asynchronous on
+ * stream s; two calls that can overlap need two workspaces. */
+int ecf8_grad_norm(const void* h_table, const void* d_table, float* d_norm, void* d_workspace, size_t workspace_bytes,
+                   int32_t* d_status, cudaStream_t s);
+
+/* ecf8_grad_norm, then out = in * min(1, max_norm / (norm + 1e-6)) for every
+ * tensor (max_norm >= 0; the product in float32, rounded once).  A norm that
+ * is not finite ORs ECF8_STATUS_NONFINITE into *d_status and the factor is 1:
+ * the gradients stay as they are, for the caller to skip the step.  Every
+ * tensor needs a d_out (ECF8_ERR_ARG). */
+int ecf8_grad_clip(const void* h_table, const void* d_table, float max_norm, float* d_norm, void* d_workspace,
+                   size_t workspace_bytes, int32_t* d_status, cudaStream_t s);
 
 /* Number of decode kernels this library has launched in this process. */
 uint64_t ecf8_launch_count(void);

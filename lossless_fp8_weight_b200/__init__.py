@@ -44,6 +44,8 @@ ERRORS = {-1: "ARG", -2: "FORMAT", -3: "CAPACITY", -4: "CODEBOOK", -5: "ALIGN", 
 STATUS_COUNT_MISMATCH = 1
 STATUS_BAD_CODE = 2
 STATUS_BAD_OFFSETS = 4
+STATUS_BAD_REQUEST = 16
+STATUS_NONFINITE = 32
 BATCH_INLINE_MAX = 64
 NOALLOC_MAX_TENSORS = 1024
 DEFAULT_CHUNK_BYTES = 32
@@ -518,3 +520,215 @@ def bf16_decode_batched(items, status=None, stream=None) -> None:
     for k, (info, d_blob, d_table, d_out) in enumerate(items):
         arr[k] = Bf16Tensor(ctypes.pointer(infos[k]), _ptr(d_blob), _ptr(d_table), _ptr(d_out))
     _check(_lib.ecf8_bf16_decode_batched(arr, len(items), _ptr(status), _stream(stream)), "ecf8_bf16_decode_batched")
+
+
+# ---- linear layers over decoded weights, with low-rank adapters ----
+
+_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+
+
+def _refuse(what: str, why: str):
+    raise Ecf8Error(-1, f"{what}: {why}")
+
+
+def _dtype_of(t, what: str) -> int:
+    d = _DTYPES.get(str(t.dtype))
+    if d is None:
+        _refuse(what, f"{t.dtype} is not bfloat16, float16 or float32")
+    return d
+
+
+def _is(t, what: str, dtype: str, shape) -> None:
+    """A contiguous tensor of this type and shape."""
+    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        _refuse(what, f"want a contiguous {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _rows(t, what: str, dtype: str, rows: int, cols: int) -> int:
+    """The row stride of a rows x cols tensor whose rows are contiguous."""
+    if str(t.dtype) != dtype or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        _refuse(what, f"want {dtype} of shape {(rows, cols)} with contiguous rows, got {t.dtype} {tuple(t.shape)}")
+    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+
+
+@dataclass
+class Adapters:
+    """Low-rank adapters of one projection: a (count, rank, in), b (count,
+    out, rank) in the activations' type, alpha (count) float32."""
+    a: object
+    b: object
+    alpha: object
+
+
+@dataclass
+class Requests:
+    """Runs of rows and the adapter of each: request i is rows offsets[i] to
+    offsets[i+1]-1 and uses adapter ids[i] (negative: none).  CUDA int32
+    tensors of count + 1 and count values."""
+    offsets: object
+    ids: object
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("d_w", _p), ("n_out", ctypes.c_uint64), ("k_in", ctypes.c_uint64), ("w_stride", ctypes.c_uint64),
+                ("d_scale", _p), ("n_scale", ctypes.c_uint64), ("d_a", _p), ("d_b", _p), ("d_alpha", _p),
+                ("n_adapters", _u32), ("rank", _u32), ("dtype", ctypes.c_int32)]
+
+
+class RequestsDesc(ctypes.Structure):
+    _fields_ = [("d_offsets", _p), ("d_ids", _p), ("count", _u32)]
+
+
+_u64 = ctypes.c_uint64
+_lib.ecf8_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDesc), _u64]
+_lib.ecf8_linear_workspace_size.restype = _sz
+_lib.ecf8_linear_forward.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(RequestsDesc), _p, _u64, _p, _u64, _u64,
+                                     _p, _p, _sz, _p, _p]
+_lib.ecf8_linear_backward.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(RequestsDesc), _p, _u64, _p, _u64, _p,
+                                      _p, _u64, _p, _p, _u64, _p, _sz, _p, _p]
+
+
+class Linear:
+    """y = scale * (x W^T) over decoded E4M3 weights, with the low-rank
+    adapters of many requests added (ecf8_linear_* in the C ABI).
+
+    ``weight`` is a CUDA uint8 tensor (out, in) with contiguous rows, or the
+    address at which a decode writes it (as ``Pipeline.acquire`` returns, plus
+    the tensor's offset) with ``shape`` given.  ``scale``: float32 CUDA tensor
+    of 1 or ``out`` values, or None.  ``dtype``: torch.bfloat16 or
+    torch.float16, the type of activations, adapters and gradients.  The
+    object keeps references and addresses; it holds no copy."""
+
+    def __init__(self, weight, shape=None, scale=None, adapters: Optional[Adapters] = None, dtype=None):
+        import torch
+        d = LinearDesc()
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if str(dtype) not in ("torch.bfloat16", "torch.float16"):
+            _refuse("Linear", f"dtype {dtype} is not bfloat16 or float16")
+        if isinstance(weight, int):
+            if shape is None:
+                _refuse("Linear", "a weight address needs a shape")
+            n, k = (int(v) for v in shape)
+            d.w_stride = k
+        else:
+            if weight.dim() != 2 or (shape is not None and tuple(shape) != tuple(weight.shape)):
+                _refuse("Linear", f"want a weight of 2 dimensions, got {tuple(weight.shape)}")
+            n, k = weight.shape
+            if weight.element_size() != 1:
+                _refuse("Linear", f"weights are E4M3 bytes, got {weight.dtype}")
+            d.w_stride = _rows(weight, "Linear weight", str(weight.dtype), n, k)
+        d.d_w, d.n_out, d.k_in, d.dtype = _ptr(weight), n, k, _DTYPES[str(dtype)]
+        if scale is not None:
+            if str(scale.dtype) != "torch.float32" or scale.numel() not in (1, n) or not scale.is_contiguous():
+                _refuse("Linear", f"scale: want 1 or {n} contiguous float32, got {scale.dtype} {tuple(scale.shape)}")
+            d.d_scale, d.n_scale = _ptr(scale), scale.numel()
+        self.rank = 0
+        if adapters is not None and adapters.a.shape[0]:
+            count, self.rank = (int(v) for v in adapters.a.shape[:2])
+            _is(adapters.a, "Linear adapters a", str(dtype), (count, self.rank, k))
+            _is(adapters.b, "Linear adapters b", str(dtype), (count, n, self.rank))
+            _is(adapters.alpha, "Linear adapters alpha", "torch.float32", (count,))
+            d.d_a, d.d_b, d.d_alpha = _ptr(adapters.a), _ptr(adapters.b), _ptr(adapters.alpha)
+            d.n_adapters, d.rank = count, self.rank
+        self.n_out, self.k_in, self.dtype = int(n), int(k), dtype
+        self._name, self._keep, self._d, self._ref = str(dtype), (weight, scale, adapters), d, ctypes.byref(d)
+
+    def workspace_size(self, rows: int) -> int:
+        """Bytes of device workspace forward and backward need for this many rows."""
+        return int(_lib.ecf8_linear_workspace_size(self._ref, rows))
+
+    def _requests(self, q):
+        if q is None:
+            return None
+        _is(q.ids, "Requests ids", "torch.int32", (q.ids.numel(),))
+        _is(q.offsets, "Requests offsets", "torch.int32", (q.ids.numel() + 1,))
+        return RequestsDesc(_ptr(q.offsets), _ptr(q.ids), q.ids.numel())
+
+    def forward(self, x, y, requests: Optional[Requests] = None, u=None, workspace=None, status=None,
+                stream=None) -> None:
+        """Asynchronously writes y (rows, out) for x (rows, in).  ``u`` (rows,
+        rank) float32 keeps A x for ``backward``."""
+        rows = x.shape[0]
+        xs = _rows(x, "Linear x", self._name, rows, self.k_in)
+        ys = _rows(y, "Linear y", self._name, rows, self.n_out)
+        if u is not None:
+            _is(u, "Linear u", "torch.float32", (rows, self.rank))
+        _check(_lib.ecf8_linear_forward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(y), ys, rows, _ptr(u),
+                                        _ptr(workspace), _nbytes(workspace, 0), _ptr(status), _stream(stream)),
+               "ecf8_linear_forward")
+
+    def backward(self, x, dy, u, dx=None, da=None, db=None, requests: Optional[Requests] = None, workspace=None,
+                 status=None, stream=None) -> None:
+        """Asynchronously writes the gradients that are given a tensor: dx
+        (rows, in), da and db (as the adapters' a and b), from dy (rows, out),
+        the forward pass's x (for da) and u (for db)."""
+        rows = dy.shape[0]
+        ds = _rows(dy, "Linear dy", self._name, rows, self.n_out)
+        xs = _rows(x, "Linear x", self._name, rows, self.k_in) if x is not None else self.k_in
+        gs = _rows(dx, "Linear dx", self._name, rows, self.k_in) if dx is not None else self.k_in
+        if u is not None:
+            _is(u, "Linear u", "torch.float32", (rows, self.rank))
+        for g, of, what in ((da, "a", "Linear da"), (db, "b", "Linear db")):
+            if g is not None:
+                if not self.rank:
+                    _refuse(what, "there are no adapters")
+                _is(g, what, self._name, getattr(self._keep[2], of).shape)
+        _check(_lib.ecf8_linear_backward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(dy), ds, _ptr(u),
+                                         _ptr(dx), gs, _ptr(da), _ptr(db), rows, _ptr(workspace),
+                                         _nbytes(workspace, 0), _ptr(status), _stream(stream)),
+               "ecf8_linear_backward")
+
+
+# ---- the global norm of a set of gradients, and clipping ----
+
+class Grad(ctypes.Structure):
+    _fields_ = [("d_in", _p), ("d_out", _p), ("n", _u64), ("dtype", ctypes.c_int32)]
+
+
+_lib.ecf8_grad_table_bytes.argtypes = [_i32]
+_lib.ecf8_grad_table_bytes.restype = _sz
+_lib.ecf8_grad_build_table.argtypes = [ctypes.POINTER(Grad), _i32, _p]
+_lib.ecf8_grad_workspace_size.restype = _sz
+_lib.ecf8_grad_norm.argtypes = [_p, _p, _p, _p, _sz, _p, _p]
+_lib.ecf8_grad_clip.argtypes = [_p, _p, ctypes.c_float, _p, _p, _sz, _p, _p]
+
+
+class GradSet:
+    """A set of gradient tensors (contiguous CUDA bfloat16, float16 or float32,
+    mixed as they come) whose global L2 norm is taken, and which are clipped by
+    it, in one call (ecf8_grad_* in the C ABI).  ``outs`` (same sizes and
+    types) receives the clipped values; by default they are written in place.
+    The descriptor table is laid out and copied to the device here, once; the
+    set's tensors must stay where they are.  Calls that can overlap on the GPU
+    need sets of their own."""
+
+    def __init__(self, grads, outs=None):
+        import torch
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            _refuse("GradSet", f"{len(grads)} tensors, {len(outs)} outputs")
+        arr = (Grad * max(1, len(grads)))()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if not g.is_contiguous() or not o.is_contiguous() or o.dtype != g.dtype or o.numel() != g.numel():
+                _refuse("GradSet", f"tensor {i}: want contiguous tensors, the output of the same type and size")
+            arr[i] = Grad(_ptr(g), _ptr(o), g.numel(), _dtype_of(g, f"GradSet tensor {i}"))
+        self._h = np.zeros(int(_lib.ecf8_grad_table_bytes(len(grads))), dtype=np.uint8)
+        _check(_lib.ecf8_grad_build_table(arr, len(grads), self._h.ctypes.data), "ecf8_grad_build_table")
+        dev = grads[0].device if grads else torch.device("cuda")
+        self._d = torch.from_numpy(self._h).to(dev)
+        self._ws = torch.empty(int(_lib.ecf8_grad_workspace_size()), dtype=torch.uint8, device=dev)
+        self._keep = (grads, outs)
+        self._args = (self._h.ctypes.data, _ptr(self._d))
+        self._ws_args = (_ptr(self._ws), self._ws.numel())
+
+    def norm(self, norm, status=None, stream=None) -> None:
+        """Asynchronously writes the L2 norm of the whole set to ``norm`` (one float32)."""
+        _check(_lib.ecf8_grad_norm(*self._args, _ptr(norm), *self._ws_args, _ptr(status), _stream(stream)),
+               "ecf8_grad_norm")
+
+    def clip(self, max_norm: float, norm, status=None, stream=None) -> None:
+        """``norm``, then every tensor times min(1, max_norm / (norm + 1e-6)).
+        A norm that is not finite sets ECF8_STATUS_NONFINITE and changes no value."""
+        _check(_lib.ecf8_grad_clip(*self._args, float(max_norm), _ptr(norm), *self._ws_args, _ptr(status),
+                                   _stream(stream)), "ecf8_grad_clip")
