@@ -95,6 +95,7 @@ extern "C" {
 /* bits OR-ed into *d_status by the linear and gradient calls */
 #define ECF8_STATUS_BAD_REQUEST 16 /* request offsets not monotone in [0, rows], or an adapter id past the last */
 #define ECF8_STATUS_NONFINITE 32   /* the norm of a gradient set is not finite */
+#define ECF8_STATUS_TIMEOUT 64     /* a kernel gave up waiting inside a launch: its output is incomplete */
 
 /* A canonical Huffman code over the 16 exponent values. */
 typedef struct ecf8_codebook {

@@ -46,6 +46,7 @@ STATUS_BAD_CODE = 2
 STATUS_BAD_OFFSETS = 4
 STATUS_BAD_REQUEST = 16
 STATUS_NONFINITE = 32
+STATUS_TIMEOUT = 64
 BATCH_INLINE_MAX = 64
 NOALLOC_MAX_TENSORS = 1024
 DEFAULT_CHUNK_BYTES = 32

@@ -14,7 +14,8 @@ CHECKED_SO = os.path.join(HERE, "libecf8_checked.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ecf8_host.cpp", "ecf8_decode.cu", "ecf8_pipeline.cpp", "ecf8_encode.cu",
                                                  "ecf8_bf16_host.cpp", "ecf8_bf16_decode.cu", "ecf8_linear.cu",
                                                  "ecf8_grad.cu")]
-HEADERS = [os.path.join(ROOT, "include", "ecf8.h"), os.path.join(CSRC, "ecf8_format.h")]
+HEADERS = [os.path.join(ROOT, "include", "ecf8.h"), os.path.join(CSRC, "ecf8_format.h"),
+           os.path.join(CSRC, "ecf8_tc.cuh")]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

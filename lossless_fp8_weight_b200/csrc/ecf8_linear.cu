@@ -12,8 +12,11 @@
 #include <cuda_runtime.h>
 
 #include "ecf8.h"
+#include "ecf8_tc.cuh"
 
 namespace {
+
+using namespace ecf8_tc;
 
 __device__ inline float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ inline float to_float(__half v) { return __half2float(v); }
@@ -141,6 +144,402 @@ __global__ void __launch_bounds__(256) product_simple(const T* q, uint64_t q_str
   }
 }
 
+// ---- the shared projection on the tensor cores ----
+//
+//     D[c][t] += sum_j W(c, j) q[t][j]        c: output (forward) or input (backward) column
+//
+// The weight is the 128-row operand and the rows of q are the other (16 to 256
+// of them), so a single token costs no more tensor work than it must and one
+// kernel serves decoding and prompts.  The tensor cores have no product of E4M3
+// by 16-bit values: eight warps widen the weights, which is exact, and put them
+// into tensor memory, from where the matrix unit reads them without passing
+// through shared memory again.  One warp loads tiles by TMA, one issues the
+// products.
+//
+// Small calls are bound by reading W: the reduction is split over a cluster of
+// up to 8 CTAs, whose sums meet in distributed shared memory in a fixed order,
+// so that few columns still occupy every SM and no workspace or second launch
+// is needed.  Large calls are bound by the matrix unit.
+
+struct ProductArgs {
+  uint64_t rows, cols;
+  uint32_t blocks;       // 64 * KB-wide steps of the reduction
+  uint32_t bt;           // rows of q in a tile, a multiple of 16, at most 256
+  uint32_t stages, split;
+  uint32_t tmem_columns, slots;
+  const float* scale;
+  uint64_t n_scale;
+  const int32_t* row_id;
+  const float* p;        // rows x rank
+  const void* f;         // the adapters' factor added to the output
+  uint64_t f_adapter, sr, sc;
+  const float* alpha;
+  uint32_t rank;         // 0: no adapters
+  uint32_t f_vector;     // 8 ranks of f are one aligned 16-byte load
+  void* out;
+  uint64_t out_stride;
+  int32_t* status;
+};
+
+constexpr int kProductThreads = 320;  // TMA, MMA and 8 widening warps
+constexpr int kWideners = 256;
+constexpr uint32_t kMaxStages = 16, kSlots = 8;
+
+// Four E4M3 bytes as two pairs of T, times 2^-120 (BF16) or 2^-8 (FP16): sign
+// and magnitude bits moved into T's places; subnormals come out as T's.
+template <class T> struct Widen;
+template <> struct Widen<__nv_bfloat16> {
+  static __device__ uint32_t pair(uint32_t v) { return ((v >> 4) & 0x07f007f0u) | (v & 0x80008000u); }
+  static __device__ uint32_t scaled(uint32_t v) {  // * 2^120, exact
+    __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&v);
+    const uint32_t k = 0x7b807b80u;
+    x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&k));
+    return *reinterpret_cast<uint32_t*>(&x);
+  }
+  static __device__ uint32_t pack(float a, float b) {
+    __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&x);
+  }
+  static constexpr uint32_t kNan = 0x7fc0;
+  static constexpr bool kBf16 = true;
+};
+template <> struct Widen<__half> {
+  static __device__ uint32_t pair(uint32_t v) { return ((v >> 1) & 0x3f803f80u) | (v & 0x80008000u); }
+  static __device__ uint32_t scaled(uint32_t v) {  // * 2^8, exact
+    __half2 x = *reinterpret_cast<__half2*>(&v);
+    const uint32_t k = 0x5c005c00u;
+    x = __hmul2(x, *reinterpret_cast<const __half2*>(&k));
+    return *reinterpret_cast<uint32_t*>(&x);
+  }
+  static __device__ uint32_t pack(float a, float b) {
+    __half2 x = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&x);
+  }
+  static constexpr uint32_t kNan = 0x7e00;
+  static constexpr bool kBf16 = false;
+};
+
+// Bits in the places of 0x80 for the bytes of w that are E4M3 NaN.
+__device__ inline uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+template <class T>
+__device__ inline void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  lo = Widen<T>::scaled(Widen<T>::pair(__byte_perm(w, 0, 0x1404)));
+  hi = Widen<T>::scaled(Widen<T>::pair(__byte_perm(w, 0, 0x3424)));
+}
+// The NaNs of w, where widen4 left finite values.
+template <class T>
+__device__ inline void widen4_nan(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t n = nan_bytes(w);
+  if (n & 0x00000080u) lo = (lo & 0xffff0000u) | Widen<T>::kNan;
+  if (n & 0x00008000u) lo = (lo & 0x0000ffffu) | Widen<T>::kNan << 16;
+  if (n & 0x00800000u) hi = (hi & 0xffff0000u) | Widen<T>::kNan;
+  if (n & 0x80000000u) hi = (hi & 0x0000ffffu) | Widen<T>::kNan << 16;
+}
+
+__device__ inline float e4m3_bits(uint32_t b) {  // value * 2^-120
+  return __uint_as_float((b & 0x80) << 24 | (b & 0x7f) << 20);
+}
+
+template <class T> __device__ inline float2 unpack(uint32_t v);
+template <> __device__ inline float2 unpack<__nv_bfloat16>(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <> __device__ inline float2 unpack<__half>(uint32_t v) {
+  return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// sum over r of p[t][r] f[a][c][r] (or f[a][r][c]): the adapter's part of one output.
+template <class T>
+__device__ inline float adapter_part(const ProductArgs& a, int32_t id, uint64_t t, uint64_t c) {
+  const float* p = a.p + t * a.rank;
+  const T* f = static_cast<const T*>(a.f) + (uint64_t)id * a.f_adapter + c * a.sc;
+  float z = 0;
+  if (a.f_vector) {
+    for (uint32_t r = 0; r < a.rank; r += 8) {
+      const uint4 w = *reinterpret_cast<const uint4*>(f + r);
+      const float4 u = *reinterpret_cast<const float4*>(p + r), v = *reinterpret_cast<const float4*>(p + r + 4);
+      float2 x = unpack<T>(w.x);
+      z = fmaf(x.x, u.x, fmaf(x.y, u.y, z));
+      x = unpack<T>(w.y);
+      z = fmaf(x.x, u.z, fmaf(x.y, u.w, z));
+      x = unpack<T>(w.z);
+      z = fmaf(x.x, v.x, fmaf(x.y, v.y, z));
+      x = unpack<T>(w.w);
+      z = fmaf(x.x, v.z, fmaf(x.y, v.w, z));
+    }
+  } else {
+    for (uint32_t r = 0; r < a.rank; ++r) z = fmaf(p[r], to_float(f[r * a.sr]), z);
+  }
+  return z * a.alpha[id];
+}
+
+template <class T, int KB, int BACK>
+__global__ void __launch_bounds__(kProductThreads)
+    product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
+               const __grid_constant__ ProductArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed_s;
+  __shared__ float max_s[8];
+  volatile int* failed = &failed_s;
+
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t w_bytes = 8192 * KB, q_bytes = a.bt * 128 * KB, stage_bytes = w_bytes + q_bytes;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
+                 freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
+  const uint64_t c0 = (uint64_t)(blockIdx.x / a.split) * 128, t0 = (uint64_t)blockIdx.y * a.bt;
+  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * crank / a.split),
+                 b1 = (uint32_t)((uint64_t)a.blocks * (crank + 1) / a.split), nb = b1 - b0;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < a.stages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 9);  // 8 widening warps and the matrix unit
+    }
+    for (uint32_t i = 0; i < a.slots; ++i) {
+      mbar_init(ready + 8 * i, 8);
+      mbar_init(freed + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    failed_s = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&tmem_base), a.tmem_columns);
+    tmem_release_permit();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base, tmem_a = tmem + (a.tmem_columns - a.slots * 32);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch(&map_w);
+      tma_prefetch(&map_q);
+      uint32_t issued = 0;
+      bool ok = true;
+      for (uint32_t i = 0; i < nb && ok; ++i) {
+        const uint32_t s = i % a.stages, turn = i / a.stages;
+        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
+          ok = false;
+          break;
+        }
+        mbar_expect(full + 8 * s, stage_bytes);
+        const uint32_t at = base + s * stage_bytes;
+        const int32_t j = (int32_t)((b0 + i) * 64 * KB);
+        if (BACK) tma_load(at, &map_w, (int32_t)c0, j, full + 8 * s);
+        else tma_load(at, &map_w, j, (int32_t)c0, full + 8 * s);
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+          tma_load(at + w_bytes + k * a.bt * 128, &map_q, j + 64 * k, (int32_t)t0, full + 8 * s);
+        ++issued;
+      }
+      // a CTA does not end while its loads are in flight
+      if (!ok)
+        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
+          const long long start = clock64();
+          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
+          }
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, a.bt);
+      uint32_t g = 0;  // 64-wide steps
+      bool ok = true;
+      for (uint32_t i = 0; i < nb && ok; ++i) {
+        const uint32_t s = i % a.stages;
+        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+#pragma unroll
+        for (int k = 0; k < KB && ok; ++k, ++g) {
+          const uint32_t slot = g % a.slots;
+          ok = mbar_wait(ready + 8 * slot, (g / a.slots) & 1, failed);
+          if (!ok) break;
+          fence_after();
+          const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * a.bt * 128);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma_ts(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
+          mma_commit(freed + 8 * slot);
+        }
+        if (ok) mma_commit(empty + 8 * s);
+      }
+      if (ok) mma_commit(done);
+    }
+  } else {
+    const int w8 = warp - 2, quarter = warp % 4, half = w8 / 4;
+    const uint32_t row = quarter * 32 + lane;
+    // with a scale for each term of the reduction the weights are scaled here, by powers of two that keep FP16 in range
+    const bool scaled = BACK && a.n_scale > 1;
+    float unit = 1.0f;
+    if (scaled && !Widen<T>::kBf16) {
+      float m = 0;
+      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += kWideners) {
+        const float s = fabsf(a.scale[i]);
+        if (s <= 3e38f) m = fmaxf(m, s);
+      }
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      if (lane == 0) max_s[w8] = m;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, max_s[i]);
+      const uint32_t e = __float_as_uint(m) >> 23;  // unit = 2^-floor(log2 m), so that m * unit is in [1, 2)
+      if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23);
+    }
+    uint32_t g = 0;
+    bool ok = true;
+    for (uint32_t i = 0; i < nb && ok; ++i) {
+      const uint32_t s = i % a.stages, at = base + s * stage_bytes;
+      ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+      ok = __all_sync(~0u, ok);
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < KB; ++k, ++g) {
+        const uint32_t slot = g % a.slots, turn = g / a.slots;
+        uint32_t v[16], bad = 0;
+        if (!BACK) {
+          uint32_t b[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t chunk = k * 4 + half * 2 + h;
+            const uint32_t off = KB == 2 ? row * 128 + ((chunk ^ (row & 7)) << 4)
+                                         : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(b[4 * h]), "=r"(b[4 * h + 1]), "=r"(b[4 * h + 2]), "=r"(b[4 * h + 3])
+                         : "r"(at + off));
+          }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            bad |= nan_bytes(b[q]);
+            widen4<T>(b[q], v[2 * q], v[2 * q + 1]);
+          }
+          if (bad)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) widen4_nan<T>(b[q], v[2 * q], v[2 * q + 1]);
+        } else {
+          const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
+          uint32_t b[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) bad |= nan_bytes(b[2 * j] | b[2 * j + 1] << 8);
+          if (!scaled) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              v[j] = Widen<T>::scaled(Widen<T>::pair(__byte_perm(b[2 * j], b[2 * j + 1], 0x4101)));
+          } else {
+            const uint64_t j0 = (uint64_t)(b0 + i) * 64 * KB + k * 64 + half * 32;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              // past the last term the scale is not read; the weights there are zeros
+              const float s0 = j0 + 2 * j < a.n_scale ? a.scale[j0 + 2 * j] * unit : 0.0f;
+              const float s1 = j0 + 2 * j + 1 < a.n_scale ? a.scale[j0 + 2 * j + 1] * unit : 0.0f;
+              v[j] = Widen<T>::pack(e4m3_bits(b[2 * j]) * 0x1p120f * s0, e4m3_bits(b[2 * j + 1]) * 0x1p120f * s1);
+            }
+          }
+          if (bad)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              uint32_t none = 0;
+              widen4_nan<T>(b[2 * j] | b[2 * j + 1] << 8, v[j], none);
+            }
+        }
+        if (turn) {
+          ok = mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          fence_after();
+        }
+        tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready + 8 * slot);
+      }
+      if (ok && lane == 0) mbar_arrive(empty + 8 * s);
+    }
+    ok = ok && mbar_wait(done, 0, failed);
+    ok = __all_sync(~0u, ok);
+    if (ok) fence_after();
+
+    const uint64_t c = c0 + row;
+    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+    float scale = 1.0f;
+    if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit : a.scale[c];
+    T* out = static_cast<T*>(a.out);
+    if (a.split == 1) {
+      if (ok)
+        for (uint32_t t = half * 16; t < a.bt; t += 32) {
+          if (t0 + t >= a.rows) break;
+          float d[16];
+          tmem_ld16(from + t, d);
+          if (c >= a.cols) continue;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t tt = t0 + t + j;
+            if (tt >= a.rows) break;
+            float y = d[j] * scale;
+            if (a.rank) {
+              const int32_t id = a.row_id[tt];
+              if (id >= 0) y += adapter_part<T>(a, id, tt, c);
+            }
+            put(out + tt * a.out_stride + c, y);
+          }
+        }
+    } else if (ok) {
+      // the tile's sums into this CTA's shared memory: every stage has been consumed
+      for (uint32_t t = half * 16; t < a.bt; t += 32) {
+        float d[16];
+        tmem_ld16(from + t, d);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((t + j) * 128 + row) * 4), "f"(d[j]) : "memory");
+      }
+    }
+  }
+  if (a.split > 1) {
+    __syncwarp();
+    cluster_sync();
+    // each CTA adds up and writes its share of the tile's rows
+    if (warp >= 2 && !*failed) {
+      const uint32_t n = threadIdx.x - 64, row = n % 128;
+      const uint64_t c = c0 + row;
+      const uint32_t lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
+      float scale = 1.0f;
+      if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f : a.scale[c];
+      if (BACK && a.n_scale > 1 && !Widen<T>::kBf16) {
+        float m = 0;
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, max_s[i]);
+        const uint32_t e = __float_as_uint(m) >> 23;
+        if (e > 0 && e < 254) scale = 1.0f / __uint_as_float((254 - e) << 23);
+      }
+      for (uint32_t t = lo + n / 128; t < hi; t += 2) {
+        const uint64_t tt = t0 + t;
+        if (tt >= a.rows || c >= a.cols) continue;
+        float y = 0;
+        for (uint32_t r = 0; r < a.split; ++r) y += cluster_ldf(base + (t * 128 + row) * 4, r);
+        y *= scale;
+        if (a.rank) {
+          const int32_t id = a.row_id[tt];
+          if (id >= 0) y += adapter_part<T>(a, id, tt, c);
+        }
+        put(static_cast<T*>(a.out) + tt * a.out_stride + c, y);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, a.tmem_columns);
+  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+}
+
 // out[a][.] = alpha[a] * sum over a's rows of p[t][r] q[t][c], element (r, c) at r * sr + c * sc.
 // One CTA an adapter, 128 columns and 8 ranks; rows in order.
 template <class T>
@@ -217,9 +616,132 @@ void route(const ecf8_linear* l, const ecf8_requests* q, uint64_t rows, int32_t*
 
 constexpr uint64_t kGridY = 65535;
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+// A map of `rows` rows of `cols` values, `stride` bytes apart, read in boxes of box_rows x box_cols.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t width, const void* at, uint64_t cols, uint64_t rows,
+              uint64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  const EncodeTiled fn = encoder();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride};
+  const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
+  (void)width;
+  return fn(map, type, 2, const_cast<void*>(at), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned(const void* p, uint64_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// TMA moves 16-byte units: bases, row strides and row lengths have to be multiples of it.  Row lengths: the map's inner
+// extent may be any, but the next row's first bytes must not be reached by a box that starts inside, which a
+// multiple of 16 values keeps out for both types.
+bool tensor_path(const ecf8_linear* l, const void* q, uint64_t q_stride) {
+  return l->k_in % 16 == 0 && l->n_out % 16 == 0 && l->k_in < (1u << 24) && l->n_out < (1u << 24) &&
+         aligned(l->d_w, 16) && l->w_stride % 16 == 0 && aligned(q, 16) && q_stride % 8 == 0;
+}
+
+template <class T, int KB, int BACK>
+int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductArgs& a, dim3 grid, size_t smem,
+                   cudaStream_t s) {
+  static bool set[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ECF8_ERR_CUDA;
+  if (dev >= 64 || !set[dev]) {
+    if (cudaFuncSetAttribute(product_tc<T, KB, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 2048) !=
+        cudaSuccess)
+      return ECF8_ERR_CUDA;
+    if (dev < 64) set[dev] = true;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, product_tc<T, KB, BACK>, mw, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
+}
+
 template <class T, int BACK>
-void product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
-             uint64_t rows, const int32_t* row_id, const float* p, cudaStream_t s) {
+int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out,
+                   uint64_t out_stride, uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status,
+                   cudaStream_t s) {
+  const uint64_t cols = BACK ? l->k_in : l->n_out, len = BACK ? l->n_out : l->k_in;
+  ProductArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
+  const int kb = a.bt <= 128 ? 2 : 1;
+  a.blocks = (uint32_t)((len + 64 * kb - 1) / (64 * kb));
+  const uint64_t tiles = (cols + 127) / 128, row_tiles = (rows + a.bt - 1) / a.bt;
+  if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
+  // Enough CTAs to keep every SM loading, while each still has a few steps to pipeline.
+  // Two CTAs share an SM where tensor memory and shared memory allow it.
+  const bool two = a.bt <= 128;
+  const uint64_t room_for = two ? 296 : 148;
+  a.split = 1;
+  while (a.split < 8 && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
+  const uint32_t stage = 8192 * kb + a.bt * 128 * kb;
+  const uint32_t room = (two ? 110 * 1024 : 200 * 1024) - 1024;
+  a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+  a.slots = two ? 4 : 8;
+  a.tmem_columns = two ? 256 : 512;
+  if (a.bt <= 128 && a.bt + a.slots * 32 > 256) return ECF8_ERR_UNSUPPORTED;
+  size_t smem = (size_t)a.stages * stage + 1024;
+  const size_t sums = (size_t)a.bt * 512 + 1024;
+  if (a.split > 1 && smem < sums) smem = sums;
+  a.scale = l->d_scale;
+  a.n_scale = l->n_scale;
+  a.row_id = row_id;
+  a.p = p;
+  a.f = BACK ? l->d_a : l->d_b;
+  a.f_adapter = (uint64_t)l->rank * cols;
+  a.sr = BACK ? l->k_in : 1;
+  a.sc = BACK ? 1 : l->rank;
+  a.alpha = l->d_alpha;
+  a.rank = adapted ? l->rank : 0;
+  a.f_vector = !BACK && l->rank % 8 == 0 && aligned(l->d_b, 16) && aligned(p, 16);
+  a.out = out;
+  a.out_stride = out_stride;
+  a.status = d_status;
+  const CUtensorMapDataType type =
+      Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mw, mq;
+  const bool made =
+      (BACK ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, l->d_w, l->k_in, l->n_out, l->w_stride, 128, 64 * kb,
+                       CU_TENSOR_MAP_SWIZZLE_NONE)
+            : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, l->d_w, l->k_in, l->n_out, l->w_stride, 64 * kb, 128,
+                       kb == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) &&
+      make_map(&mq, type, 2, in, len, rows, in_stride * 2, 64, a.bt, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (!made) return ECF8_ERR_CUDA;
+  const dim3 grid((unsigned)(tiles * a.split), (unsigned)row_tiles);
+  return kb == 2 ? product_launch<T, 2, BACK>(mw, mq, a, grid, smem, s)
+                 : product_launch<T, 1, BACK>(mw, mq, a, grid, smem, s);
+}
+
+template <class T, int BACK>
+int product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
+            uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status, cudaStream_t s) {
+  if (tensor_path(l, in, in_stride))
+    return product_tensor<T, BACK>(l, adapted, in, in_stride, out, out_stride, rows, row_id, p, d_status, s);
   const uint64_t cols = BACK ? l->k_in : l->n_out, len = BACK ? l->n_out : l->k_in;
   const uint64_t step = kGridY * 64;
   for (uint64_t t = 0; t < rows; t += step) {
@@ -230,6 +752,7 @@ void product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_str
         (uint64_t)l->rank * cols, BACK ? l->k_in : 1, BACK ? 1 : l->rank, l->d_alpha, adapted ? l->rank : 0,
         static_cast<T*>(out) + t * out_stride, out_stride);
   }
+  return ECF8_OK;
 }
 
 template <class T>
@@ -248,7 +771,8 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   } else if (l->n_adapters && keep) {
     if (cudaMemsetAsync(u, 0, rows * l->rank * 4, s) != cudaSuccess) return ECF8_ERR_CUDA;
   }
-  product<T, 0>(l, adapted, x, x_stride, y, y_stride, rows, row_id, u, s);
+  const int rc = product<T, 0>(l, adapted, x, x_stride, y, y_stride, rows, row_id, u, d_status, s);
+  if (rc) return rc;
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
@@ -266,7 +790,10 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
         static_cast<const T*>(dy), dy_stride, static_cast<const T*>(l->d_b), l->n_out * l->rank, 1, l->rank, l->n_out,
         l->rank, row_id, v);
   }
-  if (dx && rows) product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, s);
+  if (dx && rows) {
+    const int rc = product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, d_status, s);
+    if (rc) return rc;
+  }
   const uint32_t count = adapted ? q->count : 0;
   const int32_t* offsets = adapted ? q->d_offsets : nullptr;
   const int32_t* ids = adapted ? q->d_ids : nullptr;
