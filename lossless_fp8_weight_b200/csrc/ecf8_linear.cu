@@ -540,6 +540,225 @@ __global__ void __launch_bounds__(kProductThreads)
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
+// ---- x A^T of every row's own adapter, on the tensor cores ----
+//
+//     D[(adapter, r)][t] += sum_j f[adapter][r][j] q[t][j]
+//
+// Bound: one read of q.  A tile is 16 to 256 rows of q against up to 128 rows of
+// adapters: the distinct adapters of the tile's rows, `per` at a time, each
+// with its ranks on consecutive lanes.  Sums of a row with an adapter that is
+// not its own are dropped: no row sees another request's adapter.  As in the
+// projection the reduction is split over a cluster whose sums meet in
+// distributed shared memory in a fixed order.
+
+struct ShrinkArgs {
+  uint64_t rows;
+  uint32_t blocks;       // 64-wide steps of the reduction
+  uint32_t bt, stages, split;
+  uint32_t rank, per;    // ranks of an adapter, adapters in a chunk of 128 lanes
+  const int32_t* row_id;
+  float* p;              // rows x rank
+  int32_t* status;
+};
+
+constexpr int kShrinkThreads = 320;
+
+// The distinct ids >= 0 of ids[0..n), n <= 256, in the order they first occur; for threads 0..255.
+// `runs` is scratch of 256; the list and its length end in `list` and *count.  Every thread of the CTA calls it.
+__device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, int32_t* list, uint32_t* count,
+                                uint32_t* warp_sum) {
+  const uint32_t t = threadIdx.x, lane = t % 32, warp = t / 32;
+  // starts of runs of equal ids
+  bool start = t < n && ids[t] >= 0 && (t == 0 || ids[t] != ids[t - 1]);
+  uint32_t mask = __ballot_sync(~0u, start);
+  if (lane == 0 && warp < 8) warp_sum[warp] = __popc(mask);
+  __syncthreads();
+  uint32_t before = 0, total = 0;
+  for (uint32_t w = 0; w < 8; ++w) {
+    before += w < warp ? warp_sum[w] : 0;
+    total += warp_sum[w];
+  }
+  if (start) runs[before + __popc(mask & ((1u << lane) - 1))] = ids[t];
+  __syncthreads();
+  // runs whose id has not occurred before
+  bool first = t < total;
+  if (first)
+    for (uint32_t j = 0; j < t; ++j)
+      if (runs[j] == runs[t]) {
+        first = false;
+        break;
+      }
+  __syncwarp();
+  mask = __ballot_sync(~0u, first);
+  __syncthreads();
+  if (lane == 0 && warp < 8) warp_sum[warp] = __popc(mask);
+  __syncthreads();
+  before = total = 0;
+  for (uint32_t w = 0; w < 8; ++w) {
+    before += w < warp ? warp_sum[w] : 0;
+    total += warp_sum[w];
+  }
+  if (first) list[before + __popc(mask & ((1u << lane) - 1))] = runs[t];
+  if (t == 0) *count = total;
+  __syncthreads();
+}
+
+template <class T>
+__global__ void __launch_bounds__(kShrinkThreads)
+    shrink_tc(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_q,
+              const __grid_constant__ ShrinkArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed_s;
+  __shared__ int32_t ids[256], runs[256], list[256];
+  __shared__ uint32_t count_s, warp_sum[8];
+  volatile int* failed = &failed_s;
+
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t f_bytes = 16384, q_bytes = a.bt * 128, stage_bytes = f_bytes + q_bytes;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, done = empty + 8 * kMaxStages;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
+  const uint32_t chunk = blockIdx.x / a.split;
+  const uint64_t t0 = (uint64_t)blockIdx.y * a.bt;
+  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * crank / a.split),
+                 b1 = (uint32_t)((uint64_t)a.blocks * (crank + 1) / a.split), nb = b1 - b0;
+  const uint32_t columns = a.bt <= 32 ? 32 : a.bt <= 64 ? 64 : a.bt <= 128 ? 128 : 256;
+  const uint32_t pad = (a.rank + 7) / 8 * 8;
+
+  const uint32_t n = (uint32_t)(a.rows - t0 < a.bt ? a.rows - t0 : a.bt);
+  if (threadIdx.x < 256) ids[threadIdx.x] = threadIdx.x < n ? a.row_id[t0 + threadIdx.x] : -1;
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < a.stages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    failed_s = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  distinct(ids, n, runs, list, &count_s, warp_sum);
+  // rows without an adapter have zeros
+  if (chunk == 0 && crank == 0)
+    for (uint32_t t = warp; t < n; t += kShrinkThreads / 32)
+      if (ids[t] < 0)
+        for (uint32_t r = lane; r < a.rank; r += 32) a.p[(t0 + t) * a.rank + r] = 0.0f;
+  const uint32_t first = chunk * a.per;
+  if (first >= count_s) return;  // the same in every CTA of the cluster
+  const uint32_t mine = count_s - first < a.per ? count_s - first : a.per;
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&tmem_base), columns);
+    tmem_release_permit();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t issued = 0;
+      bool ok = true;
+      for (uint32_t i = 0; i < nb; ++i) {
+        const uint32_t s = i % a.stages, turn = i / a.stages;
+        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
+          ok = false;
+          break;
+        }
+        mbar_expect(full + 8 * s, q_bytes + mine * a.rank * 128);
+        const uint32_t at = base + s * stage_bytes;
+        const int32_t j = (int32_t)((b0 + i) * 64);
+        tma_load(at + f_bytes, &map_q, j, (int32_t)t0, full + 8 * s);
+        for (uint32_t k = 0; k < mine; ++k)
+          tma_load(at + k * pad * 128, &map_f, j, list[first + k] * (int32_t)a.rank, full + 8 * s);
+        ++issued;
+      }
+      // a CTA does not end while its loads are in flight
+      if (!ok)
+        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
+          const long long start = clock64();
+          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
+          }
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, a.bt);
+      bool ok = true;
+      for (uint32_t i = 0; i < nb && ok; ++i) {
+        const uint32_t s = i % a.stages;
+        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+        if (!ok) break;
+        fence_after();
+        const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) mma_ss(tmem, f + m * 2, q + m * 2, idesc, i > 0 || m > 0);
+        mma_commit(empty + 8 * s);
+      }
+      if (ok) mma_commit(done);
+    }
+  } else {
+    const int quarter = warp % 4, half = (warp - 2) / 4;
+    const uint32_t row = quarter * 32 + lane;
+    const uint32_t slot = row / pad, r = row % pad;
+    const bool ok = __all_sync(~0u, mbar_wait(done, 0, failed));
+    if (ok) {
+      fence_after();
+      const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
+      for (uint32_t t = half * 16; t < a.bt; t += 32) {
+        float d[16];
+        tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + t, d);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          if (a.split > 1)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((t + j) * 128 + row) * 4), "f"(d[j]) : "memory");
+          else if (ids[t + j] == id) a.p[(t0 + t + j) * a.rank + r] = d[j];
+        }
+      }
+    }
+  }
+  if (a.split > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && !*failed) {
+      const uint32_t k = threadIdx.x - 64, row = k % 128, slot = row / pad, r = row % pad;
+      const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
+      const uint32_t lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
+      for (uint32_t t = lo + k / 128; t < hi; t += 2) {
+        if (ids[t] != id) continue;
+        float d = 0;
+        for (uint32_t c = 0; c < a.split; ++c) d += cluster_ldf(base + (t * 128 + row) * 4, c);
+        a.p[(t0 + t) * a.rank + r] = d;
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, columns);
+  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+}
+
+// out[a][r][j] = in[a][j][r]: B with the reduction of dy B contiguous, as the kernel above reads it.
+template <class T>
+__global__ void __launch_bounds__(256) transpose_kernel(const T* in, T* out, uint64_t len, uint64_t out_len,
+                                                        uint32_t rank) {
+  __shared__ T tile[64][ECF8_RANK_MAX + 2];
+  const uint64_t j0 = (uint64_t)blockIdx.x * 64, a = blockIdx.y;
+  const uint32_t n = (uint32_t)(len - j0 < 64 ? len - j0 : 64);
+  const T* from = in + (a * len + j0) * rank;
+  for (uint32_t i = threadIdx.x; i < n * rank; i += 256) tile[i / rank][i % rank] = from[i];
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < 64 * rank; i += 256) {
+    const uint32_t r = i / 64, j = i % 64;
+    if (j < n) out[(a * rank + r) * out_len + j0 + j] = tile[j][r];
+  }
+}
+
 // out[a][.] = alpha[a] * sum over a's rows of p[t][r] q[t][c], element (r, c) at r * sr + c * sc.
 // One CTA an adapter, 128 columns and 8 ranks; rows in order.
 template <class T>
@@ -568,21 +787,24 @@ __global__ void __launch_bounds__(128) outer_simple(const float* p, uint32_t ran
       if (r < nr) put(out + (uint64_t)a * f_adapter + (r0 + r) * sr + c * sc, alpha[a] * acc[r]);
 }
 
+constexpr uint64_t kGridY = 65535;
+constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below it
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Plan {
-  size_t row_id, p, total;
+  size_t row_id, p, turned, total;
 };
 
 Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
   Plan w{};
   if (!lin->n_adapters) return w;
   w.p = up256(rows * 4);
-  w.total = w.p + up256(rows * lin->rank * 4);
+  w.turned = w.p + up256(rows * lin->rank * 4);
+  w.total = w.turned + up256((size_t)lin->n_adapters * lin->rank * lin->n_out * 2);
   return w;
 }
 
-constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below it
 
 int check(const ecf8_linear* l, const ecf8_requests* q, uint64_t rows, const void* ws, size_t ws_bytes,
           const int32_t* d_status) {
@@ -613,8 +835,6 @@ void route(const ecf8_linear* l, const ecf8_requests* q, uint64_t rows, int32_t*
   const unsigned grid = (unsigned)((most + 255) / 256 < 1024 ? (most + 255) / 256 : 1024);
   route_kernel<<<grid, 256, 0, s>>>(q->d_offsets, q->d_ids, q->count, l->n_adapters, rows, row_id, d_status);
 }
-
-constexpr uint64_t kGridY = 65535;
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -654,18 +874,22 @@ bool tensor_path(const ecf8_linear* l, const void* q, uint64_t q_stride) {
          aligned(l->d_w, 16) && l->w_stride % 16 == 0 && aligned(q, 16) && q_stride % 8 == 0;
 }
 
+template <class K>
+int allow_smem(K kernel, bool (&set)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ECF8_ERR_CUDA;
+  if (dev < 64 && set[dev]) return ECF8_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) != cudaSuccess)
+    return ECF8_ERR_CUDA;
+  if (dev < 64) set[dev] = true;
+  return ECF8_OK;
+}
+
 template <class T, int KB, int BACK>
 int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductArgs& a, dim3 grid, size_t smem,
                    cudaStream_t s) {
   static bool set[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ECF8_ERR_CUDA;
-  if (dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(product_tc<T, KB, BACK>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 2048) !=
-        cudaSuccess)
-      return ECF8_ERR_CUDA;
-    if (dev < 64) set[dev] = true;
-  }
+  if (const int rc = allow_smem(product_tc<T, KB, BACK>, set)) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kProductThreads);
@@ -737,6 +961,54 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
                  : product_launch<T, 1, BACK>(mw, mq, a, grid, smem, s);
 }
 
+// p = q f^T for every row's own adapter; f is n_adapters x rank rows of `len` values, f_stride apart.
+template <class T>
+int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint64_t f_stride, uint64_t len,
+                  uint32_t n_adapters, uint32_t rank, const int32_t* row_id, float* p, int32_t* d_status,
+                  cudaStream_t s) {
+  static bool set[64] = {};
+  if (const int rc = allow_smem(shrink_tc<T>, set)) return rc;
+  ShrinkArgs a{};
+  a.rows = rows;
+  a.blocks = (uint32_t)((len + 63) / 64);
+  a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
+  a.rank = rank;
+  a.per = 128 / ((rank + 7) / 8 * 8);
+  const uint64_t most = n_adapters < a.bt ? n_adapters : a.bt, chunks = (most + a.per - 1) / a.per,
+                 row_tiles = (rows + a.bt - 1) / a.bt;
+  if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
+  // a CTA to every SM, but at least four steps to a CTA
+  a.split = 1;
+  while (a.split < 8 && chunks * row_tiles * a.split * 2 <= 148 && a.blocks / (a.split * 2) >= 4) a.split *= 2;
+  const uint32_t stage = 16384 + a.bt * 128;
+  a.stages = (220 * 1024 - 1024) / stage < 8 ? (220 * 1024 - 1024) / stage : 8;
+  size_t smem = (size_t)a.stages * stage + 1024;
+  const size_t sums = (size_t)a.bt * 512 + 1024;
+  if (a.split > 1 && smem < sums) smem = sums;
+  a.row_id = row_id;
+  a.p = p;
+  a.status = d_status;
+  const CUtensorMapDataType type =
+      Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap mf, mq;
+  if (!make_map(&mf, type, 2, f, len, (uint64_t)n_adapters * rank, f_stride * 2, 64, rank,
+                CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&mq, type, 2, q, len, rows, q_stride * 2, 64, a.bt, CU_TENSOR_MAP_SWIZZLE_128B))
+    return ECF8_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(chunks * a.split), (unsigned)row_tiles);
+  cfg.blockDim = dim3(kShrinkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shrink_tc<T>, mf, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
+}
+
 template <class T, int BACK>
 int product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
             uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status, cudaStream_t s) {
@@ -765,9 +1037,15 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   if (l->n_adapters && !u) u = reinterpret_cast<float*>(ws + w.p);
   if (adapted) {
     route(l, q, rows, row_id, d_status, s);
-    shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
-        static_cast<const T*>(x), x_stride, static_cast<const T*>(l->d_a), l->rank * l->k_in, l->k_in, 1, l->k_in,
-        l->rank, row_id, u);
+    if (tensor_path(l, x, x_stride) && aligned(l->d_a, 16)) {
+      const int rc = shrink_tensor<T>(static_cast<const T*>(x), x_stride, rows, static_cast<const T*>(l->d_a), l->k_in,
+                                      l->k_in, l->n_adapters, l->rank, row_id, u, d_status, s);
+      if (rc) return rc;
+    } else {
+      shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
+          static_cast<const T*>(x), x_stride, static_cast<const T*>(l->d_a), l->rank * l->k_in, l->k_in, 1, l->k_in,
+          l->rank, row_id, u);
+    }
   } else if (l->n_adapters && keep) {
     if (cudaMemsetAsync(u, 0, rows * l->rank * 4, s) != cudaSuccess) return ECF8_ERR_CUDA;
   }
@@ -786,9 +1064,18 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   float* v = reinterpret_cast<float*>(ws + w.p);
   if (adapted && (dx || da)) {
     route(l, q, rows, row_id, d_status, s);
-    shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
-        static_cast<const T*>(dy), dy_stride, static_cast<const T*>(l->d_b), l->n_out * l->rank, 1, l->rank, l->n_out,
-        l->rank, row_id, v);
+    if (tensor_path(l, dy, dy_stride)) {
+      T* turned = reinterpret_cast<T*>(ws + w.turned);
+      transpose_kernel<T><<<dim3((unsigned)((l->n_out + 63) / 64), l->n_adapters), 256, 0, s>>>(
+          static_cast<const T*>(l->d_b), turned, l->n_out, l->n_out, l->rank);
+      const int rc = shrink_tensor<T>(static_cast<const T*>(dy), dy_stride, rows, turned, l->n_out, l->n_out,
+                                      l->n_adapters, l->rank, row_id, v, d_status, s);
+      if (rc) return rc;
+    } else {
+      shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
+          static_cast<const T*>(dy), dy_stride, static_cast<const T*>(l->d_b), l->n_out * l->rank, 1, l->rank,
+          l->n_out, l->rank, row_id, v);
+    }
   }
   if (dx && rows) {
     const int rc = product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, d_status, s);
