@@ -759,6 +759,271 @@ __global__ void __launch_bounds__(256) transpose_kernel(const T* in, T* out, uin
   }
 }
 
+// ---- the adapters' gradients on the tensor cores ----
+//
+//     D[c][r] = sum over the adapter's rows of q[t][c] p[t][r]
+//
+// Bound: one read of q (x for da, dy for db).  A CTA takes one adapter and 128
+// columns; q's tiles are read as TMA left them, the reduction running across
+// their rows.  p is float32 and is split into a 16-bit part and a 16-bit
+// rest, side by side as columns (2^-17 of a value is lost in BF16, 2^-22 in
+// FP16), so the rest costs columns, not another pass.  FP16 parts are taken of
+// p times a power of two that brings the adapter's largest to 2^14.  Blocks are
+// 64 rows of one request; rows past its end are cleared, since the next
+// request's may hold infinities.  Few columns split the blocks over a cluster.
+
+struct OuterArgs {
+  uint64_t rows, cols;
+  uint32_t stages, split, rank;
+  const float* p;
+  const int32_t* offsets;
+  const int32_t* ids;
+  uint32_t count;
+  const uint32_t* peak;  // FP16: bits of the largest |p| of each adapter
+  const float* alpha;
+  void* out;
+  uint64_t f_adapter, sr, sc;
+  uint32_t out_vector;   // 8 ranks of a column are one aligned 16-byte store
+  int32_t* status;
+};
+
+constexpr int kOuterThreads = 320;
+constexpr uint32_t kWindow = 320;  // requests looked through at a time
+
+template <class T>
+__device__ inline void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = Widen<T>::pack(x, y);
+  const float2 h = unpack<T>(hi);
+  // the rest of an infinity is nothing
+  lo = Widen<T>::pack(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kOuterThreads)
+    outer_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ OuterArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed_s;
+  __shared__ int32_t begin_s[kWindow], end_s[kWindow];
+  __shared__ uint32_t warp_sum[kOuterThreads / 32];
+  volatile int* failed = &failed_s;
+
+  const uint32_t pad = (a.rank + 7) / 8 * 8, n = 2 * pad;
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t q_bytes = 16384, stage_bytes = q_bytes + n * 128;
+  const uint32_t full = smem_addr(bars), ready = full + 8 * kMaxStages, empty = ready + 8 * kMaxStages,
+                 done = empty + 8 * kMaxStages;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
+  const uint64_t c0 = (uint64_t)(blockIdx.x / a.split) * 128;
+  const int32_t id = (int32_t)blockIdx.y;
+  const uint32_t columns = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < a.stages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(ready + 8 * i, 8);
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    failed_s = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&tmem_base), columns);
+    tmem_release_permit();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base;
+
+  float unit = 1.0f;  // a power of two
+  if (!Widen<T>::kBf16) {
+    const uint32_t e = a.peak[id] >> 23;  // the largest is in [2^(e-127), 2^(e-126)): to [2^13, 2^14)
+    unit = __uint_as_float((e > 14 ? 267 - e : 253) << 23);
+  }
+  const uint32_t idesc = idesc_f16(Widen<T>::kBf16, n) | kTransposeA;
+
+  uint32_t seen = 0, used = 0;  // blocks of the adapter so far; those of this CTA
+  bool ok = true;
+  for (uint32_t w0 = 0; w0 < a.count; w0 += kWindow) {
+    // this window's requests of the adapter, in order
+    const uint32_t i = w0 + threadIdx.x;
+    int32_t b = 0, e = 0;
+    if (i < a.count && a.ids[i] == id) {
+      b = max(0, a.offsets[i]);
+      e = (int32_t)min((int64_t)a.offsets[i + 1], (int64_t)a.rows);
+    }
+    const uint32_t mask = __ballot_sync(~0u, e > b);
+    if (lane == 0) warp_sum[warp] = __popc(mask);
+    __syncthreads();
+    uint32_t before = 0, total = 0;
+    for (int w = 0; w < kOuterThreads / 32; ++w) {
+      before += w < warp ? warp_sum[w] : 0;
+      total += warp_sum[w];
+    }
+    if (e > b) {
+      const uint32_t at = before + __popc(mask & ((1u << lane) - 1));
+      begin_s[at] = b;
+      end_s[at] = e;
+    }
+    __syncthreads();
+    for (uint32_t k = 0; k < total; ++k) {
+      const uint32_t blocks = (uint32_t)(end_s[k] - begin_s[k] + 63) / 64;
+      // blocks seen, seen+1, ...: those with number % split == crank are this CTA's
+      for (uint32_t j = (crank + a.split - seen % a.split) % a.split; j < blocks; j += a.split, ++used) {
+        if (!ok) continue;
+        const int64_t t0 = (int64_t)begin_s[k] + 64 * (int64_t)j;
+        const uint32_t valid = (uint32_t)min((int64_t)64, (int64_t)end_s[k] - t0);
+        const uint32_t s = used % a.stages, turn = used / a.stages, at = base + s * stage_bytes;
+        if (warp == 0) {
+          if (lane == 0) {
+            if (turn) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1, failed);
+            if (ok) {
+              mbar_expect(full + 8 * s, q_bytes);
+              tma_load(at, &map_q, (int32_t)c0, (int32_t)t0, full + 8 * s);
+              tma_load(at + 8192, &map_q, (int32_t)c0 + 64, (int32_t)t0, full + 8 * s);
+            }
+          }
+        } else if (warp == 1) {
+          if (lane == 0) {
+            ok = mbar_wait(full + 8 * s, turn & 1, failed) && mbar_wait(ready + 8 * s, turn & 1, failed);
+            if (ok) {
+              fence_after();
+              const uint64_t q = desc_mn128(at, 8192), p = desc_k128(at + q_bytes);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) mma_ss(tmem, q + m * 128, p + m * 2, idesc, used > 0 || m > 0);
+              mma_commit(empty + 8 * s);
+            }
+          }
+        } else {
+          if (turn) ok = __all_sync(~0u, mbar_wait(empty + 8 * s, (turn - 1) & 1, failed));
+          if (ok) {
+            for (uint32_t x = threadIdx.x - 64; x < a.rank * 8; x += 256) {
+              const uint32_t r = x % a.rank, t8 = x / a.rank;
+              const float* p = a.p + (uint64_t)(t0 + t8 * 8) * a.rank + r;
+              float v[8];
+#pragma unroll
+              for (uint32_t t = 0; t < 8; ++t) v[t] = t8 * 8 + t < valid ? p[t * a.rank] * unit : 0.0f;
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) split_pair<T>(v[2 * t], v[2 * t + 1], hi[t], lo[t]);
+              const uint32_t to = at + q_bytes + r * 128 + ((t8 ^ (r & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
+                           "r"(hi[3])
+                           : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + pad * 128), "r"(lo[0]), "r"(lo[1]),
+                           "r"(lo[2]), "r"(lo[3])
+                           : "memory");
+            }
+            if (valid < 64) {
+              ok = __all_sync(~0u, mbar_wait(full + 8 * s, turn & 1, failed));
+              // whole 128-byte rows, so the swizzle does not matter
+              for (uint32_t x = threadIdx.x - 64; x < (64 - valid) * 16; x += 256) {
+                const uint32_t to = at + (x / 8 % 2) * 8192 + (valid + x / 16) * 128 + x % 8 * 16;
+                if (ok) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
+              }
+            }
+            fence_async();
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(ready + 8 * s);
+          }
+        }
+      }
+      seen += blocks;
+    }
+    __syncwarp();
+    __syncthreads();
+  }
+  if (warp == 0 && lane == 0 && used) {
+    // a CTA does not end while its loads are in flight
+    if (*failed)
+      for (uint32_t i = used > a.stages ? used - a.stages : 0; i < used; ++i) {
+        const long long start = clock64();
+        while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
+        }
+      }
+  }
+  if (warp == 1 && lane == 0 && used && ok) mma_commit(done);
+  T* out = static_cast<T*>(a.out) + (uint64_t)id * a.f_adapter;
+  const float alpha = a.alpha[id] / unit;
+  if (warp >= 2) {
+    const int quarter = warp % 4, half = (warp - 2) / 4;
+    const uint32_t row = quarter * 32 + lane;
+    const uint64_t c = c0 + row;
+    if (used) {
+      ok = __all_sync(~0u, ok && mbar_wait(done, 0, failed));
+      if (ok) fence_after();
+    }
+    if (ok)
+      for (uint32_t r0 = half * 8; r0 < pad; r0 += 16) {
+        float d[8] = {}, e[8] = {};
+        if (used) {
+          tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + r0, d);
+          tmem_ld8(tmem + ((uint32_t)(quarter * 32) << 16) + pad + r0, e);
+        }
+        if (a.split > 1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((r0 + j) * 128 + row) * 4), "f"(d[j] + e[j]) : "memory");
+        } else if (c < a.cols) {
+          if (a.out_vector) {
+            uint4 v;
+            v.x = Widen<T>::pack((d[0] + e[0]) * alpha, (d[1] + e[1]) * alpha);
+            v.y = Widen<T>::pack((d[2] + e[2]) * alpha, (d[3] + e[3]) * alpha);
+            v.z = Widen<T>::pack((d[4] + e[4]) * alpha, (d[5] + e[5]) * alpha);
+            v.w = Widen<T>::pack((d[6] + e[6]) * alpha, (d[7] + e[7]) * alpha);
+            *reinterpret_cast<uint4*>(out + c * a.sc + r0) = v;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (r0 + j < a.rank) put(out + (r0 + j) * a.sr + c * a.sc, (d[j] + e[j]) * alpha);
+          }
+        }
+      }
+  }
+  if (a.split > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (warp >= 2 && !*failed) {
+      const uint32_t k = threadIdx.x - 64, row = k % 128;
+      const uint64_t c = c0 + row;
+      const uint32_t lo = a.rank * crank / a.split, hi = a.rank * (crank + 1) / a.split;
+      for (uint32_t r = lo + k / 128; r < hi; r += 2) {
+        float d = 0;
+        for (uint32_t q = 0; q < a.split; ++q) d += cluster_ldf(base + (r * 128 + row) * 4, q);
+        if (c < a.cols) put(out + r * a.sr + c * a.sc, d * alpha);
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, columns);
+  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+}
+
+// peak[a] = bits of the largest finite |p| of adapter a's rows; peak starts at zero.  The order of the maxima does not
+// matter.
+__global__ void peak_kernel(const float* p, uint64_t rows, uint32_t rank, const int32_t* row_id, uint32_t* peak) {
+  const uint64_t warps = (uint64_t)gridDim.x * blockDim.x / 32;
+  for (uint64_t t = (blockIdx.x * (uint64_t)blockDim.x + threadIdx.x) / 32; t < rows; t += warps) {
+    const int32_t id = row_id[t];
+    if (id < 0) continue;
+    float m = 0;
+    for (uint32_t r = threadIdx.x % 32; r < rank; r += 32) {
+      const float v = fabsf(p[t * rank + r]);
+      if (isfinite(v)) m = fmaxf(m, v);
+    }
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+    if (threadIdx.x % 32 == 0 && m > 0) atomicMax(peak + id, __float_as_uint(m));
+  }
+}
+
 // out[a][.] = alpha[a] * sum over a's rows of p[t][r] q[t][c], element (r, c) at r * sr + c * sc.
 // One CTA an adapter, 128 columns and 8 ranks; rows in order.
 template <class T>
@@ -793,7 +1058,7 @@ constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Plan {
-  size_t row_id, p, turned, total;
+  size_t row_id, p, turned, peak, total;
 };
 
 Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
@@ -801,7 +1066,8 @@ Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
   if (!lin->n_adapters) return w;
   w.p = up256(rows * 4);
   w.turned = w.p + up256(rows * lin->rank * 4);
-  w.total = w.turned + up256((size_t)lin->n_adapters * lin->rank * lin->n_out * 2);
+  w.peak = w.turned + up256((size_t)lin->n_adapters * lin->rank * lin->n_out * 2);
+  w.total = w.peak + up256((size_t)lin->n_adapters * 8);
   return w;
 }
 
@@ -1009,6 +1275,53 @@ int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint
   return cudaLaunchKernelEx(&cfg, shrink_tc<T>, mf, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
+// out[a] = alpha[a] * sum over a's rows of p[t] q[t], element (r, c) of an adapter at r * sr + c * sc.
+template <class T>
+int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, uint32_t rank, const ecf8_requests* req,
+                 uint64_t rows, const uint32_t* peak, const float* alpha, uint32_t n_adapters, T* out,
+                 uint64_t f_adapter, uint64_t sr, uint64_t sc, int32_t* d_status, cudaStream_t s) {
+  static bool set[64] = {};
+  if (const int rc = allow_smem(outer_tc<T>, set)) return rc;
+  OuterArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.rank = rank;
+  a.p = p;
+  a.offsets = req->d_offsets;
+  a.ids = req->d_ids;
+  a.count = req->count;
+  a.peak = peak;
+  a.alpha = alpha;
+  a.out = out;
+  a.f_adapter = f_adapter;
+  a.sr = sr;
+  a.sc = sc;
+  a.out_vector = sr == 1 && rank % 8 == 0 && aligned(out, 16);
+  a.status = d_status;
+  const uint64_t tiles = (cols + 127) / 128;
+  a.split = 1;
+  while (a.split < 8 && tiles * n_adapters * a.split * 2 <= 148 && rows / (64 * a.split * 2) >= 2) a.split *= 2;
+  const uint32_t pad = (rank + 7) / 8 * 8, stage = 16384 + pad * 256;
+  a.stages = (220 * 1024 - 1024) / stage < 8 ? (220 * 1024 - 1024) / stage : 8;
+  const size_t smem = (size_t)a.stages * stage + 1024;  // at least the sums, pad * 512 bytes
+  CUtensorMap mq;
+  if (!make_map(&mq, Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, cols,
+                rows, q_stride * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return ECF8_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * a.split), n_adapters);
+  cfg.blockDim = dim3(kOuterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, outer_tc<T>, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
+}
+
 template <class T, int BACK>
 int product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
             uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status, cudaStream_t s) {
@@ -1062,8 +1375,8 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   const Plan w = plan_of(l, rows);
   int32_t* row_id = reinterpret_cast<int32_t*>(ws);
   float* v = reinterpret_cast<float*>(ws + w.p);
+  if (adapted) route(l, q, rows, row_id, d_status, s);
   if (adapted && (dx || da)) {
-    route(l, q, rows, row_id, d_status, s);
     if (tensor_path(l, dy, dy_stride)) {
       T* turned = reinterpret_cast<T*>(ws + w.turned);
       transpose_kernel<T><<<dim3((unsigned)((l->n_out + 63) / 64), l->n_adapters), 256, 0, s>>>(
@@ -1084,14 +1397,34 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   const uint32_t count = adapted ? q->count : 0;
   const int32_t* offsets = adapted ? q->d_offsets : nullptr;
   const int32_t* ids = adapted ? q->d_ids : nullptr;
-  if (da)
+  const bool fp16 = l->dtype == ECF8_DTYPE_FP16;
+  uint32_t* peak = reinterpret_cast<uint32_t*>(ws + w.peak);  // of v, then of u
+  const bool da_tensor = da && adapted && tensor_path(l, x, x_stride), db_tensor = db && adapted && tensor_path(l, dy, dy_stride);
+  if (fp16 && (da_tensor || db_tensor)) {
+    if (cudaMemsetAsync(peak, 0, (size_t)l->n_adapters * 8, s) != cudaSuccess) return ECF8_ERR_CUDA;
+    const unsigned grid = (unsigned)((rows + 7) / 8 < 592 ? (rows + 7) / 8 : 592);
+    if (da_tensor) peak_kernel<<<grid, 256, 0, s>>>(v, rows, l->rank, row_id, peak);
+    if (db_tensor) peak_kernel<<<grid, 256, 0, s>>>(u, rows, l->rank, row_id, peak + l->n_adapters);
+  }
+  if (da_tensor) {
+    const int rc = outer_tensor<T>(static_cast<const T*>(x), x_stride, l->k_in, v, l->rank, q, rows, peak, l->d_alpha,
+                                   l->n_adapters, static_cast<T*>(da), l->rank * l->k_in, l->k_in, 1, d_status, s);
+    if (rc) return rc;
+  } else if (da) {
     outer_simple<T><<<dim3((unsigned)((l->k_in + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
         v, l->rank, static_cast<const T*>(x), x_stride, l->k_in, offsets, ids, count, rows, l->d_alpha,
         static_cast<T*>(da), l->rank * l->k_in, l->k_in, 1);
-  if (db)
+  }
+  if (db_tensor) {
+    const int rc = outer_tensor<T>(static_cast<const T*>(dy), dy_stride, l->n_out, u, l->rank, q, rows,
+                                   peak + l->n_adapters, l->d_alpha, l->n_adapters, static_cast<T*>(db),
+                                   l->rank * l->n_out, 1, l->rank, d_status, s);
+    if (rc) return rc;
+  } else if (db) {
     outer_simple<T><<<dim3((unsigned)((l->n_out + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
         u, l->rank, static_cast<const T*>(dy), dy_stride, l->n_out, offsets, ids, count, rows, l->d_alpha,
         static_cast<T*>(db), l->rank * l->n_out, 1, l->rank);
+  }
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 

@@ -105,6 +105,14 @@ __device__ inline uint64_t desc_k128(uint32_t addr) {
          (uint64_t)2 << 61;
 }
 
+// Shared-memory operand of 128-byte rows along the output dimension (64 values of 16 bits), one row for each term
+// of the reduction, 128-byte swizzle: 8-row groups 1024 bytes apart, the next 64 values `next` bytes apart.
+__device__ inline uint64_t desc_mn128(uint32_t addr, uint32_t next) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+constexpr uint32_t kTransposeA = 1u << 15;  // in the instruction descriptor: A is desc_mn128
+
 // 16-bit inputs of one type, float32 sums, 128 x n; both operands with the reduction contiguous.
 __host__ __device__ inline uint32_t idesc_f16(bool bf16, uint32_t n) {
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
@@ -126,6 +134,14 @@ __device__ inline void tmem_ld16(uint32_t tmem, float (&v)[16]) {
       "tcgen05.wait::ld.sync.aligned;"
       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
         "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(tmem)
+      : "memory");
+}
+__device__ inline void tmem_ld8(uint32_t tmem, float (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
       : "r"(tmem)
       : "memory");
 }
