@@ -151,94 +151,74 @@ __global__ void __launch_bounds__(256) product_simple(const T* q, uint64_t q_str
 // The weight is the 128-row operand and the rows of q are the other (16 to 256
 // of them), so a single token costs no more tensor work than it must and one
 // kernel serves decoding and prompts.  The tensor cores have no product of E4M3
-// by 16-bit values: eight warps widen the weights, which is exact, and put them
+// by 16-bit values: warps widen the weights, which is exact, and put them
 // into tensor memory, from where the matrix unit reads them without passing
 // through shared memory again.  One warp loads tiles by TMA, one issues the
 // products.
 //
-// Small calls are bound by reading W: the reduction is split over a cluster of
-// up to 8 CTAs, whose sums meet in distributed shared memory in a fixed order,
-// so that few columns still occupy every SM and no workspace or second launch
-// is needed.  Large calls are bound by the matrix unit.
+// Small calls (up to 128 rows) are bound by reading W: the reduction is split
+// over a cluster of up to 8 CTAs, whose sums meet in distributed shared memory
+// in a fixed order, so that few columns still occupy every SM and no workspace
+// or second launch is needed.  Large calls are bound by the matrix unit and by
+// what L2 can deliver: two CTAs act as one on a 256 x 256 tile, each loading
+// its own weights and half of q.
+//
+// The adapters' part of large calls is more terms of the same sum,
+//     D[c][t] += sum over the tile's adapters a, ranks r of (f[a][c][r] alpha[a] / s[c]) * [a is t's] p[t][r],
+// 32 terms for 16 ranks of an adapter: both factors as a BF16 value and a BF16
+// rest (three products; 2^-16 of a term is lost).  Factors of either side that are
+// not finite are left out of it and their terms added one by one at the end,
+// where they meet their own rows only and no rest; so are columns whose scale
+// is zero or extreme.
 
-struct ProductArgs {
-  uint64_t rows, cols;
-  uint32_t blocks;       // 64 * KB-wide steps of the reduction
-  uint32_t bt;           // rows of q in a tile, a multiple of 16, at most 256
-  uint32_t stages, split;
-  uint32_t tmem_columns, slots;
-  const float* scale;
-  uint64_t n_scale;
-  const int32_t* row_id;
-  const float* p;        // rows x rank
-  const void* f;         // the adapters' factor added to the output
-  uint64_t f_adapter, sr, sc;
-  const float* alpha;
-  uint32_t rank;         // 0: no adapters
-  uint32_t f_vector;     // 8 ranks of f are one aligned 16-byte load
-  void* out;
-  uint64_t out_stride;
-  int32_t* status;
+// Two E4M3 bytes in bits 0-7 and 16-23 as a pair of T.  BF16: the sign to bit
+// 15, the magnitude to T's exponent and upper mantissa bits (subnormals come
+// out as T's), which is the value times 2^-120, and one exact product.  The
+// integer pipe and the multiply pipe both run at 64 lanes a clock (measured),
+// and all shifts on the first bound the widening; so the shifts are
+// multiplications, by factors that the compiler does not know (it would make
+// them shifts again).  FP16 has a conversion, 32 lanes a clock.
+struct WidenBy {
+  uint32_t magnitude;  // 16
+  uint32_t sign;       // 256
+  uint32_t one;        // 1
 };
-
-constexpr int kProductThreads = 320;  // TMA, MMA and 8 widening warps
-constexpr int kWideners = 256;
-constexpr uint32_t kMaxStages = 16, kSlots = 8;
-
-// Four E4M3 bytes as two pairs of T, times 2^-120 (BF16) or 2^-8 (FP16): sign
-// and magnitude bits moved into T's places; subnormals come out as T's.
 template <class T> struct Widen;
 template <> struct Widen<__nv_bfloat16> {
-  static __device__ uint32_t pair(uint32_t v) { return ((v >> 4) & 0x07f007f0u) | (v & 0x80008000u); }
-  static __device__ uint32_t scaled(uint32_t v) {  // * 2^120, exact
-    __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&v);
-    const uint32_t k = 0x7b807b80u;
-    x = __hmul2(x, *reinterpret_cast<const __nv_bfloat162*>(&k));
-    return *reinterpret_cast<uint32_t*>(&x);
-  }
   static __device__ uint32_t pack(float a, float b) {
     __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&x);
   }
-  static constexpr uint32_t kNan = 0x7fc0;
   static constexpr bool kBf16 = true;
 };
 template <> struct Widen<__half> {
-  static __device__ uint32_t pair(uint32_t v) { return ((v >> 1) & 0x3f803f80u) | (v & 0x80008000u); }
-  static __device__ uint32_t scaled(uint32_t v) {  // * 2^8, exact
-    __half2 x = *reinterpret_cast<__half2*>(&v);
-    const uint32_t k = 0x5c005c00u;
-    x = __hmul2(x, *reinterpret_cast<const __half2*>(&k));
-    return *reinterpret_cast<uint32_t*>(&x);
-  }
   static __device__ uint32_t pack(float a, float b) {
     __half2 x = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&x);
   }
-  static constexpr uint32_t kNan = 0x7e00;
   static constexpr bool kBf16 = false;
 };
 
-// Bits in the places of 0x80 for the bytes of w that are E4M3 NaN.
-__device__ inline uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-template <class T>
-__device__ inline void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  lo = Widen<T>::scaled(Widen<T>::pair(__byte_perm(w, 0, 0x1404)));
-  hi = Widen<T>::scaled(Widen<T>::pair(__byte_perm(w, 0, 0x3424)));
+// `top` gets a bit of kNanTop where a magnitude is 0x7f (NaN), which comes out as a finite value.
+constexpr uint32_t kNanTop = 0x08000800u;
+__device__ inline uint32_t widen2_bf16(uint32_t p, const WidenBy& by, uint32_t& top) {
+  const uint32_t m = (p * by.magnitude) & 0x07f007f0u;
+  top = m * by.one + 0x00100010u;
+  const uint32_t v = m | ((p * by.sign) & 0x80008000u), k = 0x7b807b80u;  // 2^120
+  const __nv_bfloat162 x =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&x);
 }
-// The NaNs of w, where widen4 left finite values.
-template <class T>
-__device__ inline void widen4_nan(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t n = nan_bytes(w);
-  if (n & 0x00000080u) lo = (lo & 0xffff0000u) | Widen<T>::kNan;
-  if (n & 0x00008000u) lo = (lo & 0x0000ffffu) | Widen<T>::kNan << 16;
-  if (n & 0x00800000u) hi = (hi & 0xffff0000u) | Widen<T>::kNan;
-  if (n & 0x80000000u) hi = (hi & 0x0000ffffu) | Widen<T>::kNan << 16;
+__device__ inline uint32_t widen2_nan(uint32_t p, uint32_t v) {
+  if ((p & 0x7f) == 0x7f) v = (v & 0xffff0000u) | 0x7fc0u;
+  if ((p & 0x7f0000) == 0x7f0000) v = (v & 0x0000ffffu) | 0x7fc00000u;
+  return v;
 }
-
-__device__ inline float e4m3_bits(uint32_t b) {  // value * 2^-120
-  return __uint_as_float((b & 0x80) << 24 | (b & 0x7f) << 20);
+// Two E4M3 bytes next to each other as a pair of FP16.
+__device__ inline uint32_t widen2_fp16(uint32_t b) {
+  uint32_t v;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(v) : "r"(b));
+  return v;
 }
 
 template <class T> __device__ inline float2 unpack(uint32_t v);
@@ -249,321 +229,16 @@ template <> __device__ inline float2 unpack<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-// sum over r of p[t][r] f[a][c][r] (or f[a][r][c]): the adapter's part of one output.
+// Two values as a pair of T and the pair of their rests.
 template <class T>
-__device__ inline float adapter_part(const ProductArgs& a, int32_t id, uint64_t t, uint64_t c) {
-  const float* p = a.p + t * a.rank;
-  const T* f = static_cast<const T*>(a.f) + (uint64_t)id * a.f_adapter + c * a.sc;
-  float z = 0;
-  if (a.f_vector) {
-    for (uint32_t r = 0; r < a.rank; r += 8) {
-      const uint4 w = *reinterpret_cast<const uint4*>(f + r);
-      const float4 u = *reinterpret_cast<const float4*>(p + r), v = *reinterpret_cast<const float4*>(p + r + 4);
-      float2 x = unpack<T>(w.x);
-      z = fmaf(x.x, u.x, fmaf(x.y, u.y, z));
-      x = unpack<T>(w.y);
-      z = fmaf(x.x, u.z, fmaf(x.y, u.w, z));
-      x = unpack<T>(w.z);
-      z = fmaf(x.x, v.x, fmaf(x.y, v.y, z));
-      x = unpack<T>(w.w);
-      z = fmaf(x.x, v.z, fmaf(x.y, v.w, z));
-    }
-  } else {
-    for (uint32_t r = 0; r < a.rank; ++r) z = fmaf(p[r], to_float(f[r * a.sr]), z);
-  }
-  return z * a.alpha[id];
+__device__ inline void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = Widen<T>::pack(x, y);
+  const float2 h = unpack<T>(hi);
+  // the rest of an infinity is nothing
+  lo = Widen<T>::pack(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
 }
 
-template <class T, int KB, int BACK>
-__global__ void __launch_bounds__(kProductThreads)
-    product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
-               const __grid_constant__ ProductArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
-  __shared__ uint32_t tmem_base;
-  __shared__ int failed_s;
-  __shared__ float max_s[8];
-  volatile int* failed = &failed_s;
-
-  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
-  const uint32_t w_bytes = 8192 * KB, q_bytes = a.bt * 128 * KB, stage_bytes = w_bytes + q_bytes;
-  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
-                 freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
-  const uint64_t c0 = (uint64_t)(blockIdx.x / a.split) * 128, t0 = (uint64_t)blockIdx.y * a.bt;
-  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * crank / a.split),
-                 b1 = (uint32_t)((uint64_t)a.blocks * (crank + 1) / a.split), nb = b1 - b0;
-
-  if (threadIdx.x == 0) {
-    for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 9);  // 8 widening warps and the matrix unit
-    }
-    for (uint32_t i = 0; i < a.slots; ++i) {
-      mbar_init(ready + 8 * i, 8);
-      mbar_init(freed + 8 * i, 1);
-    }
-    mbar_init(done, 1);
-    failed_s = 0;
-    mbar_init_fence();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_addr(&tmem_base), a.tmem_columns);
-    tmem_release_permit();
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = tmem_base, tmem_a = tmem + (a.tmem_columns - a.slots * 32);
-
-  if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch(&map_w);
-      tma_prefetch(&map_q);
-      uint32_t issued = 0;
-      bool ok = true;
-      for (uint32_t i = 0; i < nb && ok; ++i) {
-        const uint32_t s = i % a.stages, turn = i / a.stages;
-        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
-          ok = false;
-          break;
-        }
-        mbar_expect(full + 8 * s, stage_bytes);
-        const uint32_t at = base + s * stage_bytes;
-        const int32_t j = (int32_t)((b0 + i) * 64 * KB);
-        if (BACK) tma_load(at, &map_w, (int32_t)c0, j, full + 8 * s);
-        else tma_load(at, &map_w, j, (int32_t)c0, full + 8 * s);
-#pragma unroll
-        for (int k = 0; k < KB; ++k)
-          tma_load(at + w_bytes + k * a.bt * 128, &map_q, j + 64 * k, (int32_t)t0, full + 8 * s);
-        ++issued;
-      }
-      // a CTA does not end while its loads are in flight
-      if (!ok)
-        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
-          const long long start = clock64();
-          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
-          }
-        }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, a.bt);
-      uint32_t g = 0;  // 64-wide steps
-      bool ok = true;
-      for (uint32_t i = 0; i < nb && ok; ++i) {
-        const uint32_t s = i % a.stages;
-        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
-#pragma unroll
-        for (int k = 0; k < KB && ok; ++k, ++g) {
-          const uint32_t slot = g % a.slots;
-          ok = mbar_wait(ready + 8 * slot, (g / a.slots) & 1, failed);
-          if (!ok) break;
-          fence_after();
-          const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * a.bt * 128);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) mma_ts(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
-          mma_commit(freed + 8 * slot);
-        }
-        if (ok) mma_commit(empty + 8 * s);
-      }
-      if (ok) mma_commit(done);
-    }
-  } else {
-    const int w8 = warp - 2, quarter = warp % 4, half = w8 / 4;
-    const uint32_t row = quarter * 32 + lane;
-    // with a scale for each term of the reduction the weights are scaled here, by powers of two that keep FP16 in range
-    const bool scaled = BACK && a.n_scale > 1;
-    float unit = 1.0f;
-    if (scaled && !Widen<T>::kBf16) {
-      float m = 0;
-      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += kWideners) {
-        const float s = fabsf(a.scale[i]);
-        if (s <= 3e38f) m = fmaxf(m, s);
-      }
-      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-      if (lane == 0) max_s[w8] = m;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, max_s[i]);
-      const uint32_t e = __float_as_uint(m) >> 23;  // unit = 2^-floor(log2 m), so that m * unit is in [1, 2)
-      if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23);
-    }
-    uint32_t g = 0;
-    bool ok = true;
-    for (uint32_t i = 0; i < nb && ok; ++i) {
-      const uint32_t s = i % a.stages, at = base + s * stage_bytes;
-      ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
-      ok = __all_sync(~0u, ok);
-      if (!ok) break;
-#pragma unroll
-      for (int k = 0; k < KB; ++k, ++g) {
-        const uint32_t slot = g % a.slots, turn = g / a.slots;
-        uint32_t v[16], bad = 0;
-        if (!BACK) {
-          uint32_t b[8];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t chunk = k * 4 + half * 2 + h;
-            const uint32_t off = KB == 2 ? row * 128 + ((chunk ^ (row & 7)) << 4)
-                                         : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(b[4 * h]), "=r"(b[4 * h + 1]), "=r"(b[4 * h + 2]), "=r"(b[4 * h + 3])
-                         : "r"(at + off));
-          }
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            bad |= nan_bytes(b[q]);
-            widen4<T>(b[q], v[2 * q], v[2 * q + 1]);
-          }
-          if (bad)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) widen4_nan<T>(b[q], v[2 * q], v[2 * q + 1]);
-        } else {
-          const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
-          uint32_t b[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
-#pragma unroll
-          for (int j = 0; j < 16; ++j) bad |= nan_bytes(b[2 * j] | b[2 * j + 1] << 8);
-          if (!scaled) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              v[j] = Widen<T>::scaled(Widen<T>::pair(__byte_perm(b[2 * j], b[2 * j + 1], 0x4101)));
-          } else {
-            const uint64_t j0 = (uint64_t)(b0 + i) * 64 * KB + k * 64 + half * 32;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              // past the last term the scale is not read; the weights there are zeros
-              const float s0 = j0 + 2 * j < a.n_scale ? a.scale[j0 + 2 * j] * unit : 0.0f;
-              const float s1 = j0 + 2 * j + 1 < a.n_scale ? a.scale[j0 + 2 * j + 1] * unit : 0.0f;
-              v[j] = Widen<T>::pack(e4m3_bits(b[2 * j]) * 0x1p120f * s0, e4m3_bits(b[2 * j + 1]) * 0x1p120f * s1);
-            }
-          }
-          if (bad)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint32_t none = 0;
-              widen4_nan<T>(b[2 * j] | b[2 * j + 1] << 8, v[j], none);
-            }
-        }
-        if (turn) {
-          ok = mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed);
-          ok = __all_sync(~0u, ok);
-          if (!ok) break;
-          fence_after();
-        }
-        tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
-        wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(ready + 8 * slot);
-      }
-      if (ok && lane == 0) mbar_arrive(empty + 8 * s);
-    }
-    ok = ok && mbar_wait(done, 0, failed);
-    ok = __all_sync(~0u, ok);
-    if (ok) fence_after();
-
-    const uint64_t c = c0 + row;
-    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
-    float scale = 1.0f;
-    if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit : a.scale[c];
-    T* out = static_cast<T*>(a.out);
-    if (a.split == 1) {
-      if (ok)
-        for (uint32_t t = half * 16; t < a.bt; t += 32) {
-          if (t0 + t >= a.rows) break;
-          float d[16];
-          tmem_ld16(from + t, d);
-          if (c >= a.cols) continue;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t tt = t0 + t + j;
-            if (tt >= a.rows) break;
-            float y = d[j] * scale;
-            if (a.rank) {
-              const int32_t id = a.row_id[tt];
-              if (id >= 0) y += adapter_part<T>(a, id, tt, c);
-            }
-            put(out + tt * a.out_stride + c, y);
-          }
-        }
-    } else if (ok) {
-      // the tile's sums into this CTA's shared memory: every stage has been consumed
-      for (uint32_t t = half * 16; t < a.bt; t += 32) {
-        float d[16];
-        tmem_ld16(from + t, d);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((t + j) * 128 + row) * 4), "f"(d[j]) : "memory");
-      }
-    }
-  }
-  if (a.split > 1) {
-    __syncwarp();
-    cluster_sync();
-    // each CTA adds up and writes its share of the tile's rows
-    if (warp >= 2 && !*failed) {
-      const uint32_t n = threadIdx.x - 64, row = n % 128;
-      const uint64_t c = c0 + row;
-      const uint32_t lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
-      float scale = 1.0f;
-      if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f : a.scale[c];
-      if (BACK && a.n_scale > 1 && !Widen<T>::kBf16) {
-        float m = 0;
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, max_s[i]);
-        const uint32_t e = __float_as_uint(m) >> 23;
-        if (e > 0 && e < 254) scale = 1.0f / __uint_as_float((254 - e) << 23);
-      }
-      for (uint32_t t = lo + n / 128; t < hi; t += 2) {
-        const uint64_t tt = t0 + t;
-        if (tt >= a.rows || c >= a.cols) continue;
-        float y = 0;
-        for (uint32_t r = 0; r < a.split; ++r) y += cluster_ldf(base + (t * 128 + row) * 4, r);
-        y *= scale;
-        if (a.rank) {
-          const int32_t id = a.row_id[tt];
-          if (id >= 0) y += adapter_part<T>(a, id, tt, c);
-        }
-        put(static_cast<T*>(a.out) + tt * a.out_stride + c, y);
-      }
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its sums
-  }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  if (warp == 1) tmem_free(tmem, a.tmem_columns);
-  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
-}
-
-// ---- x A^T of every row's own adapter, on the tensor cores ----
-//
-//     D[(adapter, r)][t] += sum_j f[adapter][r][j] q[t][j]
-//
-// Bound: one read of q.  A tile is 16 to 256 rows of q against up to 128 rows of
-// adapters: the distinct adapters of the tile's rows, `per` at a time, each
-// with its ranks on consecutive lanes.  Sums of a row with an adapter that is
-// not its own are dropped: no row sees another request's adapter.  As in the
-// projection the reduction is split over a cluster whose sums meet in
-// distributed shared memory in a fixed order.
-
-struct ShrinkArgs {
-  uint64_t rows;
-  uint32_t blocks;       // 64-wide steps of the reduction
-  uint32_t bt, stages, split;
-  uint32_t rank, per;    // ranks of an adapter, adapters in a chunk of 128 lanes
-  const int32_t* row_id;
-  float* p;              // rows x rank
-  int32_t* status;
-};
-
-constexpr int kShrinkThreads = 320;
-
-// The distinct ids >= 0 of ids[0..n), n <= 256, in the order they first occur; for threads 0..255.
+// The distinct ids >= 0 of ids[0..n), n <= 256, in the order they first occur, by threads 0..255.
 // `runs` is scratch of 256; the list and its length end in `list` and *count.  Every thread of the CTA calls it.
 __device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, int32_t* list, uint32_t* count,
                                 uint32_t* warp_sum) {
@@ -602,6 +277,540 @@ __device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, i
   if (t == 0) *count = total;
   __syncthreads();
 }
+
+struct ProductArgs {
+  uint64_t rows, cols, len;
+  uint32_t blocks;       // 64 * KB-wide steps of the reduction
+  uint32_t bt;           // rows of q in a tile, a multiple of 16, at most 256
+  uint32_t stages, split;
+  const float* scale;
+  uint64_t n_scale;
+  const int32_t* row_id;
+  const float* p;        // rows x rank
+  const void* f;         // the adapters' factor added to the output
+  uint64_t f_adapter, sr, sc;
+  const float* alpha;
+  uint32_t rank;         // 0: no adapters
+  uint32_t f_vector;     // 8 ranks of f are one aligned 16-byte load
+  uint32_t p_vector;     // and 4 of p
+  void* out;
+  uint64_t out_stride;
+  int32_t* status;
+  WidenBy by;
+};
+
+constexpr uint32_t kMaxStages = 16, kSlots = 8;
+
+// sum over r of p[t][r] f[a][c][r] (or f[a][r][c]): the adapter's part of one output.
+template <class T>
+__device__ inline float adapter_part(const ProductArgs& a, int32_t id, uint64_t t, uint64_t c, uint32_t r0,
+                                     uint32_t r1) {
+  const float* p = a.p + t * a.rank;
+  const T* f = static_cast<const T*>(a.f) + (uint64_t)id * a.f_adapter + c * a.sc;
+  float z = 0;
+  if (a.f_vector && a.p_vector) {
+    for (uint32_t r = r0; r < r1; r += 8) {
+      const uint4 w = *reinterpret_cast<const uint4*>(f + r);
+      const float4 u = *reinterpret_cast<const float4*>(p + r), v = *reinterpret_cast<const float4*>(p + r + 4);
+      float2 x = unpack<T>(w.x);
+      z = fmaf(x.x, u.x, fmaf(x.y, u.y, z));
+      x = unpack<T>(w.y);
+      z = fmaf(x.x, u.z, fmaf(x.y, u.w, z));
+      x = unpack<T>(w.z);
+      z = fmaf(x.x, v.x, fmaf(x.y, v.y, z));
+      x = unpack<T>(w.w);
+      z = fmaf(x.x, v.z, fmaf(x.y, v.w, z));
+    }
+  } else {
+    for (uint32_t r = r0; r < r1; ++r) z = fmaf(p[r], to_float(f[r * a.sr]), z);
+  }
+  return z * a.alpha[id];
+}
+
+// 16 ranks of the factor of column c from rank r0 on, times `by`; false if one is not finite.
+template <class T>
+__device__ inline bool adapter_factor(const ProductArgs& a, int32_t id, uint64_t c, uint32_t r0, float by,
+                                      float (&v)[16]) {
+  const T* f = static_cast<const T*>(a.f) + (uint64_t)id * a.f_adapter + c * a.sc;
+  if (a.f_vector) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r0 + 8 * h < a.rank) w = *reinterpret_cast<const uint4*>(f + r0 + 8 * h);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 y = unpack<T>(x[k]);
+        v[8 * h + 2 * k] = y.x * by;
+        v[8 * h + 2 * k + 1] = y.y * by;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = r0 + k < a.rank ? to_float(f[(r0 + k) * a.sr]) * by : 0.0f;
+  }
+  float m = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) m = fmaxf(m, v[k] != v[k] ? INFINITY : fabsf(v[k]));
+  return m < 3e38f;
+}
+
+// 16 of a row's p from rank r0 on; false if one is not finite.
+__device__ inline bool row_factor(const ProductArgs& a, uint64_t t, uint32_t r0, float (&y)[16]) {
+  const float* p = a.p + t * a.rank;
+  if (a.p_vector) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float4 z = make_float4(0, 0, 0, 0);
+      if (r0 + 4 * q < a.rank) z = *reinterpret_cast<const float4*>(p + r0 + 4 * q);
+      y[4 * q] = z.x;
+      y[4 * q + 1] = z.y;
+      y[4 * q + 2] = z.z;
+      y[4 * q + 3] = z.w;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) y[q] = r0 + q < a.rank ? p[r0 + q] : 0.0f;
+  }
+  float m = 0;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) m = fmaxf(m, y[q] != y[q] ? INFINITY : fabsf(y[q]));
+  return m < 3e38f;
+}
+
+// The ranks of an adapter's part that the tensor cores left out.
+template <class T>
+__device__ float left_out(const ProductArgs& a, int32_t id, uint64_t t, uint64_t c, float scale, bool divides) {
+  float z = 0;
+  for (uint32_t r0 = 0; r0 < a.rank; r0 += 16) {
+    float f[16], y[16];
+    const bool fits = adapter_factor<T>(a, id, c, r0, a.alpha[id] / scale, f);
+    if (!row_factor(a, t, r0, y) || !fits || !divides)
+      z += adapter_part<T>(a, id, t, c, r0, r0 + 16 < a.rank ? r0 + 16 : a.rank);
+  }
+  return z;
+}
+
+// P: CTAs of a tile.  KB: 64-wide steps in a stage.  G: groups of 8 widening warps.
+template <class T, int P, int KB, int G, int BACK>
+__global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
+    product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
+               const __grid_constant__ ProductArgs a) {
+  constexpr uint32_t slots = P == 2 ? 8 : 4, columns = P == 2 ? 512 : 256;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int failed_s;
+  __shared__ float unit_s;
+  __shared__ float max_s[8 * G];
+  __shared__ __align__(16) float scale_s[BACK ? 8 * G : 1][32];
+  __shared__ int32_t ids[256], runs[256], list[256];
+  __shared__ uint32_t count_s, warp_sum[8], apart_s;
+  volatile int* failed = &failed_s;
+
+  const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t rows_here = a.bt / P;  // rows of q that this CTA loads
+  const uint32_t w_bytes = 8192 * KB, q_bytes = rows_here * 128 * KB, stage_bytes = w_bytes + q_bytes;
+  const uint32_t pair_base = base + a.stages * stage_bytes;  // P = 2: the adapters' operand, G of rows_here * 128 bytes
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
+                 freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t cluster = P * a.split, crank = cluster > 1 ? cluster_rank() : 0;
+  const uint32_t side = crank % P, part = crank / P, leader = part * P;
+  const uint64_t c0 = ((uint64_t)(blockIdx.x / cluster) * P + side) * 128, t0 = (uint64_t)blockIdx.y * a.bt;
+  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * part / a.split),
+                 b1 = (uint32_t)((uint64_t)a.blocks * (part + 1) / a.split), nb = b1 - b0;
+  const uint32_t steps = nb * KB;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < a.stages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 8 * (G < KB ? G : KB) + 1);  // the warps that read it and the matrix unit
+    }
+    for (uint32_t i = 0; i < slots; ++i) {
+      mbar_init(ready + 8 * i, 8 * P);
+      mbar_init(freed + 8 * i, 1);
+    }
+    mbar_init(done, 1);
+    failed_s = 0;
+    apart_s = 0;
+    unit_s = 1.0f;
+    count_s = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) {
+    tmem_alloc<P>(smem_addr(&tmem_base), columns);
+    tmem_release_permit<P>();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base, tmem_a = tmem + (columns - slots * 32);
+  uint32_t adapter_steps = 0, units = 0;
+  if (P == 2) {
+    // the other CTA's barriers are ready before anything arrives on them
+    cluster_sync();
+    if (a.rank) {
+      if (threadIdx.x < 256) ids[threadIdx.x] = threadIdx.x < a.bt && t0 + threadIdx.x < a.rows ? a.row_id[t0 + threadIdx.x] : -1;
+      __syncthreads();
+      distinct(ids, a.bt, runs, list, &count_s, warp_sum);
+      units = count_s * ((a.rank + 15) / 16);
+      const uint32_t all = (units + 1) / 2;  // steps of two units, dealt out to the parts
+      adapter_steps = all / a.split + (part < all % a.split ? 1 : 0);
+    }
+  }
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch(&map_w);
+      tma_prefetch(&map_q);
+      uint32_t issued = 0;
+      bool ok = true;
+      for (uint32_t i = 0; i < nb; ++i) {
+        const uint32_t s = i % a.stages, turn = i / a.stages;
+        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
+          ok = false;
+          break;
+        }
+        mbar_expect(full + 8 * s, stage_bytes);
+        const uint32_t at = base + s * stage_bytes;
+        const int32_t j = (int32_t)((b0 + i) * 64 * KB);
+        if (BACK) tma_load(at, &map_w, (int32_t)c0, j, full + 8 * s);
+        else tma_load(at, &map_w, j, (int32_t)c0, full + 8 * s);
+#pragma unroll
+        for (int k = 0; k < KB; ++k)
+          tma_load(at + w_bytes + k * rows_here * 128, &map_q, j + 64 * k, (int32_t)(t0 + side * rows_here), full + 8 * s);
+        ++issued;
+      }
+      // a CTA does not end while its loads are in flight
+      if (!ok)
+        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
+          const long long start = clock64();
+          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
+          }
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && side == 0) {
+      const uint32_t mask = 3u << leader;
+      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128 * P, a.bt);
+      uint32_t g = 0;  // 64-wide steps
+      bool ok = true;
+      for (uint32_t i = 0; i < nb && ok; ++i) {
+        const uint32_t s = i % a.stages;
+        // the other CTA's warps have waited for its tiles before they report a step ready
+        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+#pragma unroll
+        for (int k = 0; k < KB && ok; ++k, ++g) {
+          const uint32_t slot = g % slots;
+          ok = mbar_wait<P == 2>(ready + 8 * slot, (g / slots) & 1, failed);
+          if (!ok) break;
+          fence_after();
+          const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * rows_here * 128);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
+          mma_commit<P>(freed + 8 * slot, mask);
+        }
+        if (ok) mma_commit<P>(empty + 8 * s, mask);
+      }
+      if (P == 2) {
+        const uint32_t idesc_pair = idesc_f16(true, 128 * P, a.bt);
+        for (uint32_t i = 0; i < adapter_steps && ok; ++i, ++g) {
+          const uint32_t slot = g % slots;
+          ok = mbar_wait<true>(ready + 8 * slot, (g / slots) & 1, failed);
+          if (!ok) break;
+          fence_after();
+          const uint64_t b = desc_k128(pair_base + (g % G) * rows_here * 128);
+          const uint32_t first = (i * a.split + part) * 2;
+          for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
+            const uint32_t hi = tmem_a + slot * 32 + u * 16;
+            mma_ts<P>(tmem, hi, b + u * 4, idesc_pair, g > 0 || u > 0);
+            mma_ts<P>(tmem, hi, b + u * 4 + 2, idesc_pair, 1);
+            mma_ts<P>(tmem, hi + 8, b + u * 4, idesc_pair, 1);
+          }
+          mma_commit<P>(freed + 8 * slot, mask);
+        }
+      }
+      if (ok) mma_commit<P>(done, mask);
+    }
+  } else {
+    const int w8 = warp - 2, quarter = warp % 4, half = w8 / 4 % 2, group = w8 / 8;
+    const uint32_t row = quarter * 32 + lane;
+    const uint64_t c = c0 + row;
+    // with a scale for each term of the reduction the weights are scaled here, by powers of two that keep FP16 in range
+    const bool scaled = BACK && a.n_scale > 1;
+    float unit = 1.0f;
+    if (scaled && !Widen<T>::kBf16) {
+      float m = 0;
+      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += 256 * G) {
+        const float s = fabsf(a.scale[i]);
+        if (s <= 3e38f) m = fmaxf(m, s);
+      }
+      for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+      if (lane == 0) max_s[w8] = m;
+      asm volatile("bar.sync 1, %0;" ::"n"(256 * G) : "memory");
+      for (int i = 0; i < 8 * G; ++i) m = fmaxf(m, max_s[i]);
+      const uint32_t e = __float_as_uint(m) >> 23;  // unit = 2^-floor(log2 m), so that m * unit is in [1, 2)
+      if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23);
+      if (threadIdx.x == 64) unit_s = unit;
+    }
+    // the output's scale, and whether the adapters' factors may be divided by it
+    float scale = 1.0f;
+    if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit : a.scale[c];
+    const bool divides = fabsf(scale) >= 0x1p-40f && fabsf(scale) <= 0x1p40f;
+
+    // Group `group` of 8 warps takes every G-th 64-wide step.  A step's store is waited for, and announced, only when
+    // the next one has been widened, which hides its latency.
+    uint32_t pending = ~0u;
+    auto announce = [&] {
+      wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (P == 2 && side) mbar_arrive_at(ready + 8 * pending, leader);
+        else mbar_arrive(ready + 8 * pending);
+      }
+    };
+    bool ok = true;
+    uint32_t g = group;
+    for (; g < steps; g += G) {
+      const uint32_t i = g / KB, k = g % KB, s = i % a.stages, at = base + s * stage_bytes;
+      const uint32_t slot = g % slots, turn = g / slots;
+      if (scaled) {
+        // past the last term the scale is not read; the weights there are zeros
+        const uint64_t j = (uint64_t)b0 * 64 * KB + (uint64_t)g * 64 + half * 32 + lane;
+        const float v = j < a.n_scale ? a.scale[j] * unit : 0.0f;
+        __syncwarp();
+        scale_s[BACK ? w8 : 0][lane] = v;
+        __syncwarp();
+      }
+      ok = __all_sync(~0u, mbar_wait(full + 8 * s, (i / a.stages) & 1, failed));
+      if (!ok) break;
+      uint32_t v[16];
+      if (!BACK) {
+        uint32_t b[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t chunk = k * 4 + half * 2 + h;
+          const uint32_t off = KB == 2 ? row * 128 + ((chunk ^ (row & 7)) << 4)
+                                       : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(b[4 * h]), "=r"(b[4 * h + 1]), "=r"(b[4 * h + 2]), "=r"(b[4 * h + 3])
+                       : "r"(at + off));
+        }
+        if (Widen<T>::kBf16) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint32_t n0, n1;
+            v[2 * q] = widen2_bf16(__byte_perm(b[q], 0, 0x4140), a.by, n0);
+            v[2 * q + 1] = widen2_bf16(__byte_perm(b[q], 0, 0x4342), a.by, n1);
+            bad |= n0 | n1;
+          }
+          if (bad & kNanTop)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              v[2 * q] = widen2_nan(__byte_perm(b[q], 0, 0x4140), v[2 * q]);
+              v[2 * q + 1] = widen2_nan(__byte_perm(b[q], 0, 0x4342), v[2 * q + 1]);
+            }
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            v[2 * q] = widen2_fp16(b[q]);
+            v[2 * q + 1] = widen2_fp16(b[q] >> 16);
+          }
+        }
+      } else {
+        const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
+        uint32_t b[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
+        if (Widen<T>::kBf16) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            uint32_t n;
+            v[j] = widen2_bf16(b[2 * j + 1] * 65536u + b[2 * j], a.by, n);
+            bad |= n;
+          }
+          if (bad & kNanTop)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = widen2_nan(b[2 * j + 1] * 65536u + b[2 * j], v[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = widen2_fp16(b[2 * j + 1] * 256u + b[2 * j]);
+        }
+        if (scaled)
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w8 : 0][2 * j]);
+            const float2 w = unpack<T>(v[j]), z = unpack<T>(v[j + 1]);
+            v[j] = Widen<T>::pack(w.x * x.x, w.y * x.y);
+            v[j + 1] = Widen<T>::pack(z.x * x.z, z.y * x.w);
+          }
+      }
+      __syncwarp();
+      if (lane == 0 && (G >= KB || k == KB - 1)) mbar_arrive(empty + 8 * s);
+      if (pending != ~0u) announce();
+      if (turn) {
+        ok = __all_sync(~0u, mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed));
+        if (!ok) break;
+        fence_after();
+      }
+      tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
+      pending = slot;
+    }
+    if (ok && pending != ~0u) announce();
+
+    if (P == 2) {
+      // Adapter steps: each half of a group widens one unit's factors; together they write the rows' side of both.
+      const uint32_t chunks = (a.rank + 15) / 16;
+      for (; g < steps + adapter_steps && ok; g += G) {
+        const uint32_t slot = g % slots, turn = g / slots, first = ((g - steps) * a.split + part) * 2;
+        // this slot is free; and so is the group's operand buffer, whose last reader was the step G before
+        if (turn) ok = __all_sync(~0u, mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed));
+        if (ok && g >= steps + G)
+          ok = __all_sync(~0u, mbar_wait(freed + 8 * ((g - G) % slots), ((g - G) / slots) & 1, failed));
+        if (!ok) break;
+        fence_after();
+        uint32_t v[16] = {};
+        if (first + half < units) {
+          const int32_t id = list[(first + half) / chunks];
+          float f[16];
+          bool fits = c < a.cols && divides;
+          if (c < a.cols) fits = adapter_factor<T>(a, id, c, (first + half) % chunks * 16, a.alpha[id] / scale, f) && fits;
+          if (fits)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(f[2 * q], f[2 * q + 1], v[q], v[8 + q]);
+          else if (c < a.cols) apart_s = 0x3f800000u;
+        }
+        tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
+        const uint32_t to = pair_base + (g % G) * rows_here * 128;
+        for (uint32_t x = threadIdx.x - 64 - group * 256; x < rows_here * 2; x += 256) {
+          const uint32_t t = x / 2, u = x % 2;
+          const uint64_t tt = t0 + side * rows_here + t;
+          uint32_t hi[8] = {}, lo[8] = {};
+          if (first + u < units && ids[side * rows_here + t] == list[(first + u) / chunks]) {
+            float y[16];
+            if (row_factor(a, tt, (first + u) % chunks * 16, y)) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(y[2 * q], y[2 * q + 1], hi[q], lo[q]);
+            } else {
+              for (uint32_t r = 0; r < 2; ++r) cluster_stu(smem_addr(&apart_s), leader + r, 0x3f800000u);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t* z = q < 2 ? hi + 4 * q : lo + 4 * (q - 2);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + t * 128 + (((u * 4 + q) ^ (t & 7)) << 4)),
+                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3])
+                         : "memory");
+          }
+        }
+        fence_async();
+        pending = slot;
+        announce();
+      }
+    }
+    ok = ok && mbar_wait(done, 0, failed);
+    ok = __all_sync(~0u, ok);
+    if (ok) fence_after();
+    if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(256 * G) : "memory");  // apart_s
+
+    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+    T* out = static_cast<T*>(a.out);
+    if (a.split == 1) {
+      const bool apart = P == 2 && apart_s;
+      if (ok)
+        for (uint32_t t = (group * 2 + half) * 16; t < a.bt; t += 32 * G) {
+          if (t0 + t >= a.rows) break;
+          float d[16];
+          tmem_ld16(from + t, d);
+          if (c >= a.cols) continue;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t tt = t0 + t + j;
+            if (tt >= a.rows) break;
+            float y = d[j] * scale;
+            if (a.rank && (P == 1 || apart)) {
+              const int32_t id = P == 1 ? a.row_id[tt] : ids[t + j];
+              if (id >= 0) y += P == 1 ? adapter_part<T>(a, id, tt, c, 0, a.rank) : left_out<T>(a, id, tt, c, scale, divides);
+            }
+            put(out + tt * a.out_stride + c, y);
+          }
+        }
+    } else if (ok) {
+      // the tile's sums into this CTA's shared memory: every stage has been consumed
+      for (uint32_t t = (group * 2 + half) * 16; t < a.bt; t += 32 * G) {
+        float d[16];
+        tmem_ld16(from + t, d);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((t + j) * 128 + row) * 4), "f"(d[j]) : "memory");
+      }
+    }
+  }
+  if (a.split > 1) {
+    __syncwarp();
+    cluster_sync();
+    // each CTA adds up and writes its share of the tile's rows
+    if (warp >= 2 && !*failed) {
+      const uint32_t n = threadIdx.x - 64, row = n % 128;
+      const uint64_t c = c0 + row;
+      const uint32_t lo = a.bt * part / a.split, hi = a.bt * (part + 1) / a.split;
+      float scale = 1.0f;
+      if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit_s : a.scale[c];
+      const bool divides = fabsf(scale) >= 0x1p-40f && fabsf(scale) <= 0x1p40f;
+      bool apart = false;
+      if (P == 2)
+        for (uint32_t r = 0; r < a.split; ++r) apart |= cluster_ldf(smem_addr(&apart_s), r * P + side) != 0.0f;
+      for (uint32_t t = lo + n / 128; t < hi; t += 2 * G) {
+        const uint64_t tt = t0 + t;
+        if (tt >= a.rows || c >= a.cols) continue;
+        float y = 0;
+        for (uint32_t r = 0; r < a.split; ++r) y += cluster_ldf(base + (t * 128 + row) * 4, r * P + side);
+        y *= scale;
+        if (a.rank && (P == 1 || apart)) {
+          const int32_t id = P == 1 ? a.row_id[tt] : ids[t];
+          if (id >= 0) y += P == 1 ? adapter_part<T>(a, id, tt, c, 0, a.rank) : left_out<T>(a, id, tt, c, scale, divides);
+        }
+        put(static_cast<T*>(a.out) + tt * a.out_stride + c, y);
+      }
+    }
+  }
+  if (cluster > 1) {
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free<P>(tmem, columns);
+  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+}
+
+// ---- x A^T of every row's own adapter, on the tensor cores ----
+//
+//     D[(adapter, r)][t] += sum_j f[adapter][r][j] q[t][j]
+//
+// Bound: one read of q.  A tile is 16 to 256 rows of q against up to 128 rows of
+// adapters: the distinct adapters of the tile's rows, `per` at a time, each
+// with its ranks on consecutive lanes.  Sums of a row with an adapter that is
+// not its own are dropped: no row sees another request's adapter.  As in the
+// projection the reduction is split over a cluster whose sums meet in
+// distributed shared memory in a fixed order.
+
+struct ShrinkArgs {
+  uint64_t rows;
+  uint32_t blocks;       // 64-wide steps of the reduction
+  uint32_t bt, stages, split;
+  uint32_t rank, per;    // ranks of an adapter, adapters in a chunk of 128 lanes
+  const int32_t* row_id;
+  float* p;              // rows x rank
+  int32_t* status;
+};
+
+constexpr int kShrinkThreads = 320;
 
 template <class T>
 __global__ void __launch_bounds__(kShrinkThreads)
@@ -649,8 +858,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   if (first >= count_s) return;  // the same in every CTA of the cluster
   const uint32_t mine = count_s - first < a.per ? count_s - first : a.per;
   if (warp == 1) {
-    tmem_alloc(smem_addr(&tmem_base), columns);
-    tmem_release_permit();
+    tmem_alloc<1>(smem_addr(&tmem_base), columns);
+    tmem_release_permit<1>();
   }
   fence_before();
   __syncthreads();
@@ -685,7 +894,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, a.bt);
+      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, a.bt);
       bool ok = true;
       for (uint32_t i = 0; i < nb && ok; ++i) {
         const uint32_t s = i % a.stages;
@@ -695,9 +904,9 @@ __global__ void __launch_bounds__(kShrinkThreads)
         const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
 #pragma unroll
         for (int m = 0; m < 4; ++m) mma_ss(tmem, f + m * 2, q + m * 2, idesc, i > 0 || m > 0);
-        mma_commit(empty + 8 * s);
+        mma_commit<1>(empty + 8 * s, 0);
       }
-      if (ok) mma_commit(done);
+      if (ok) mma_commit<1>(done, 0);
     }
   } else {
     const int quarter = warp % 4, half = (warp - 2) / 4;
@@ -739,7 +948,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 1) tmem_free(tmem, columns);
+  if (warp == 1) tmem_free<1>(tmem, columns);
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
@@ -791,14 +1000,6 @@ constexpr int kOuterThreads = 320;
 constexpr uint32_t kWindow = 320;  // requests looked through at a time
 
 template <class T>
-__device__ inline void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = Widen<T>::pack(x, y);
-  const float2 h = unpack<T>(hi);
-  // the rest of an infinity is nothing
-  lo = Widen<T>::pack(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
-}
-
-template <class T>
 __global__ void __launch_bounds__(kOuterThreads)
     outer_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ OuterArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -831,8 +1032,8 @@ __global__ void __launch_bounds__(kOuterThreads)
     mbar_init_fence();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(&tmem_base), columns);
-    tmem_release_permit();
+    tmem_alloc<1>(smem_addr(&tmem_base), columns);
+    tmem_release_permit<1>();
   }
   fence_before();
   __syncthreads();
@@ -844,7 +1045,7 @@ __global__ void __launch_bounds__(kOuterThreads)
     const uint32_t e = a.peak[id] >> 23;  // the largest is in [2^(e-127), 2^(e-126)): to [2^13, 2^14)
     unit = __uint_as_float((e > 14 ? 267 - e : 253) << 23);
   }
-  const uint32_t idesc = idesc_f16(Widen<T>::kBf16, n) | kTransposeA;
+  const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, n) | kTransposeA;
 
   uint32_t seen = 0, used = 0;  // blocks of the adapter so far; those of this CTA
   bool ok = true;
@@ -895,7 +1096,7 @@ __global__ void __launch_bounds__(kOuterThreads)
               const uint64_t q = desc_mn128(at, 8192), p = desc_k128(at + q_bytes);
 #pragma unroll
               for (int m = 0; m < 4; ++m) mma_ss(tmem, q + m * 128, p + m * 2, idesc, used > 0 || m > 0);
-              mma_commit(empty + 8 * s);
+              mma_commit<1>(empty + 8 * s, 0);
             }
           }
         } else {
@@ -946,7 +1147,7 @@ __global__ void __launch_bounds__(kOuterThreads)
         }
       }
   }
-  if (warp == 1 && lane == 0 && used && ok) mma_commit(done);
+  if (warp == 1 && lane == 0 && used && ok) mma_commit<1>(done, 0);
   T* out = static_cast<T*>(a.out) + (uint64_t)id * a.f_adapter;
   const float alpha = a.alpha[id] / unit;
   if (warp >= 2) {
@@ -1003,7 +1204,7 @@ __global__ void __launch_bounds__(kOuterThreads)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 1) tmem_free(tmem, columns);
+  if (warp == 1) tmem_free<1>(tmem, columns);
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
@@ -1119,13 +1320,12 @@ EncodeTiled encoder() {
 }
 
 // A map of `rows` rows of `cols` values, `stride` bytes apart, read in boxes of box_rows x box_cols.
-bool make_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t width, const void* at, uint64_t cols, uint64_t rows,
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* at, uint64_t cols, uint64_t rows,
               uint64_t stride, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
   const EncodeTiled fn = encoder();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride};
   const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
-  (void)width;
   return fn(map, type, 2, const_cast<void*>(at), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1145,29 +1345,29 @@ int allow_smem(K kernel, bool (&set)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ECF8_ERR_CUDA;
   if (dev < 64 && set[dev]) return ECF8_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 222 * 1024) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
     return ECF8_ERR_CUDA;
   if (dev < 64) set[dev] = true;
   return ECF8_OK;
 }
 
-template <class T, int KB, int BACK>
+template <class T, int P, int KB, int G, int BACK>
 int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductArgs& a, dim3 grid, size_t smem,
                    cudaStream_t s) {
   static bool set[64] = {};
-  if (const int rc = allow_smem(product_tc<T, KB, BACK>, set)) return rc;
+  if (const int rc = allow_smem(product_tc<T, P, KB, G, BACK>, set)) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kProductThreads);
+  cfg.blockDim = dim3(64 + 256 * G);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = a.split;
+  attr[0].val.clusterDim.x = P * a.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, product_tc<T, KB, BACK>, mw, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, product_tc<T, P, KB, G, BACK>, mw, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
 template <class T, int BACK>
@@ -1178,24 +1378,22 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   ProductArgs a{};
   a.rows = rows;
   a.cols = cols;
+  a.len = len;
   a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
-  const int kb = a.bt <= 128 ? 2 : 1;
+  const bool pair = a.bt > 128;  // two CTAs to a tile; else two CTAs to an SM
+  const int kb = pair ? 1 : 2, width = pair ? 2 : 1, groups = pair ? 2 : 1;
   a.blocks = (uint32_t)((len + 64 * kb - 1) / (64 * kb));
-  const uint64_t tiles = (cols + 127) / 128, row_tiles = (rows + a.bt - 1) / a.bt;
+  const uint64_t tiles = (cols + 128 * width - 1) / (128 * width), row_tiles = (rows + a.bt - 1) / a.bt;
   if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
   // Enough CTAs to keep every SM loading, while each still has a few steps to pipeline.
-  // Two CTAs share an SM where tensor memory and shared memory allow it.
-  const bool two = a.bt <= 128;
-  const uint64_t room_for = two ? 296 : 148;
+  const uint64_t room_for = pair ? 74 : 296;
+  const uint32_t most = 8 / width;
   a.split = 1;
-  while (a.split < 8 && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
-  const uint32_t stage = 8192 * kb + a.bt * 128 * kb;
-  const uint32_t room = (two ? 110 * 1024 : 200 * 1024) - 1024;
+  while (a.split < most && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
+  const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb, pairs = pair ? groups * here * 128 : 0;
+  const uint32_t room = (pair ? 216 * 1024 - pairs : 106 * 1024) - 1024;
   a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-  a.slots = two ? 4 : 8;
-  a.tmem_columns = two ? 256 : 512;
-  if (a.bt <= 128 && a.bt + a.slots * 32 > 256) return ECF8_ERR_UNSUPPORTED;
-  size_t smem = (size_t)a.stages * stage + 1024;
+  size_t smem = (size_t)a.stages * stage + pairs + 1024;
   const size_t sums = (size_t)a.bt * 512 + 1024;
   if (a.split > 1 && smem < sums) smem = sums;
   a.scale = l->d_scale;
@@ -1208,23 +1406,25 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.sc = BACK ? 1 : l->rank;
   a.alpha = l->d_alpha;
   a.rank = adapted ? l->rank : 0;
-  a.f_vector = !BACK && l->rank % 8 == 0 && aligned(l->d_b, 16) && aligned(p, 16);
+  a.f_vector = !BACK && l->rank % 8 == 0 && aligned(l->d_b, 16);
+  a.p_vector = l->rank % 4 == 0 && aligned(p, 16);
   a.out = out;
   a.out_stride = out_stride;
   a.status = d_status;
+  a.by = WidenBy{16, 256, 1};
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mw, mq;
   const bool made =
-      (BACK ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, l->d_w, l->k_in, l->n_out, l->w_stride, 128, 64 * kb,
+      (BACK ? make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, l->d_w, l->k_in, l->n_out, l->w_stride, 128, 64 * kb,
                        CU_TENSOR_MAP_SWIZZLE_NONE)
-            : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, l->d_w, l->k_in, l->n_out, l->w_stride, 64 * kb, 128,
+            : make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, l->d_w, l->k_in, l->n_out, l->w_stride, 64 * kb, 128,
                        kb == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B)) &&
-      make_map(&mq, type, 2, in, len, rows, in_stride * 2, 64, a.bt, CU_TENSOR_MAP_SWIZZLE_128B);
+      make_map(&mq, type, in, len, rows, in_stride * 2, 64, here, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!made) return ECF8_ERR_CUDA;
-  const dim3 grid((unsigned)(tiles * a.split), (unsigned)row_tiles);
-  return kb == 2 ? product_launch<T, 2, BACK>(mw, mq, a, grid, smem, s)
-                 : product_launch<T, 1, BACK>(mw, mq, a, grid, smem, s);
+  const dim3 grid((unsigned)(tiles * width * a.split), (unsigned)row_tiles);
+  return pair ? product_launch<T, 2, 1, 2, BACK>(mw, mq, a, grid, smem, s)
+              : product_launch<T, 1, 2, 1, BACK>(mw, mq, a, grid, smem, s);
 }
 
 // p = q f^T for every row's own adapter; f is n_adapters x rank rows of `len` values, f_stride apart.
@@ -1257,9 +1457,9 @@ int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mf, mq;
-  if (!make_map(&mf, type, 2, f, len, (uint64_t)n_adapters * rank, f_stride * 2, 64, rank,
+  if (!make_map(&mf, type, f, len, (uint64_t)n_adapters * rank, f_stride * 2, 64, rank,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map(&mq, type, 2, q, len, rows, q_stride * 2, 64, a.bt, CU_TENSOR_MAP_SWIZZLE_128B))
+      !make_map(&mq, type, q, len, rows, q_stride * 2, 64, a.bt, CU_TENSOR_MAP_SWIZZLE_128B))
     return ECF8_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(chunks * a.split), (unsigned)row_tiles);
@@ -1305,7 +1505,7 @@ int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, u
   a.stages = (220 * 1024 - 1024) / stage < 8 ? (220 * 1024 - 1024) / stage : 8;
   const size_t smem = (size_t)a.stages * stage + 1024;  // at least the sums, pad * 512 bytes
   CUtensorMap mq;
-  if (!make_map(&mq, Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, q, cols,
+  if (!make_map(&mq, Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, cols,
                 rows, q_stride * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
     return ECF8_ERR_CUDA;
   cudaLaunchConfig_t cfg{};

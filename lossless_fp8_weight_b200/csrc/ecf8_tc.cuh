@@ -26,28 +26,50 @@ __device__ inline void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ inline void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Arrives on the barrier at this offset of another CTA of the cluster.
+__device__ inline void mbar_arrive_at(uint32_t bar, uint32_t rank) {
+  asm volatile(
+      "{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n"
+      " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(bar),
+      "r"(rank)
+      : "memory");
+}
+// CLUSTER: another CTA's arrivals are among those waited for.
+template <bool CLUSTER = false>
 __device__ inline bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 // Waits for the phase of this parity to complete; false when the limit ran out
-// or another wait of the CTA has failed.
+// or another wait of the CTA has failed.  The clock is read rarely: waiting
+// warps should leave the issue slots to the working ones.
+template <bool CLUSTER = false>
 __device__ inline bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
-  if (mbar_try(bar, parity)) return true;
+  if (mbar_try<CLUSTER>(bar, parity)) return true;
   const long long start = clock64();
-  while (!mbar_try(bar, parity)) {
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try<CLUSTER>(bar, parity)) return true;
     if (*failed) return false;
     if (clock64() - start > kWaitCycles) {
       *failed = 1;
       return false;
     }
   }
-  return true;
 }
 
 __device__ inline void tma_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -60,15 +82,29 @@ __device__ inline void tma_prefetch(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// P: CTAs that act as one, 1 or 2.  With 2, both CTAs of a pair allocate and free; one thread of the even CTA
+// issues the products, whose 128 output rows a CTA lie in its own tensor memory and whose other operand comes half
+// from each CTA's shared memory; a commit arrives on the barriers at this offset of every CTA in `mask`.
+template <int P>
 __device__ inline void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
-               : "memory");
+  if constexpr (P == 1)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+                 : "memory");
+  else
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+                 : "memory");
 }
+template <int P>
 __device__ inline void tmem_release_permit() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  if constexpr (P == 1) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  else asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
+template <int P>
 __device__ inline void tmem_free(uint32_t tmem, uint32_t columns) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+  if constexpr (P == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
 }
 __device__ inline void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ inline void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -77,17 +113,32 @@ __device__ inline void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;"
 __device__ inline void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Arrives on bar once every matrix product issued so far by this thread has ended.
-__device__ inline void mma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+template <int P>
+__device__ inline void mma_commit(uint32_t bar, uint32_t mask) {
+  if constexpr (P == 1)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+                     "r"(bar),
+                 "h"((uint16_t)mask)
+                 : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 128 x n x 16.
+// D[tmem] (+)= A[tmem] * B[smem], 128 * P x n x 16.
+template <int P>
 __device__ inline void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (P == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 // D[tmem] (+)= A[smem] * B[smem], 128 x n x 16.
 __device__ inline void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -113,9 +164,9 @@ __device__ inline uint64_t desc_mn128(uint32_t addr, uint32_t next) {
 }
 constexpr uint32_t kTransposeA = 1u << 15;  // in the instruction descriptor: A is desc_mn128
 
-// 16-bit inputs of one type, float32 sums, 128 x n; both operands with the reduction contiguous.
-__host__ __device__ inline uint32_t idesc_f16(bool bf16, uint32_t n) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (n >> 3) << 17 | (128u >> 4) << 24;
+// 16-bit inputs of one type, float32 sums, m x n; both operands with the reduction contiguous.
+__host__ __device__ inline uint32_t idesc_f16(bool bf16, uint32_t m, uint32_t n) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
 __device__ inline void tmem_st16(uint32_t tmem, const uint32_t (&v)[16]) {
@@ -161,6 +212,11 @@ __device__ inline float cluster_ldf(uint32_t addr, uint32_t rank) {
                : "r"(addr), "r"(rank)
                : "memory");
   return v;
+}
+__device__ inline void cluster_stu(uint32_t addr, uint32_t rank, uint32_t v) {
+  asm volatile("{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.u32 [a], %2;\n}" ::"r"(addr),
+               "r"(rank), "r"(v)
+               : "memory");
 }
 
 }  // namespace ecf8_tc
