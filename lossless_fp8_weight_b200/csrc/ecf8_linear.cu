@@ -278,6 +278,17 @@ __device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, i
   __syncthreads();
 }
 
+// A CTA does not end while its loads are in flight.  The next use of a stage would have been `s` with parity `turn`:
+// waits, with a limit, for the last use of every stage (at once where it has ended, or where there was none).
+__device__ inline void drain(uint32_t full, uint32_t s, uint32_t turn, uint32_t stages) {
+  for (uint32_t i = 0; i < stages; ++i) {
+    const uint32_t last = i < s ? turn : turn ^ 1;
+    const long long start = clock64();
+    while (!mbar_try(full + 8 * i, last) && clock64() - start < kWaitCycles) {
+    }
+  }
+}
+
 struct ProductArgs {
   uint64_t rows, cols, len;
   uint32_t blocks;       // 64 * KB-wide steps of the reduction
@@ -391,9 +402,9 @@ __device__ float left_out(const ProductArgs& a, int32_t id, uint64_t t, uint64_t
   return z;
 }
 
-// P: CTAs of a tile.  KB: 64-wide steps in a stage.  G: groups of 8 widening warps.
+// P: CTAs of a tile.  KB: 64-wide steps in a stage.  G: groups of 4 widening warps.
 template <class T, int P, int KB, int G, int BACK>
-__global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
+__global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
                const __grid_constant__ ProductArgs a) {
   constexpr uint32_t slots = P == 2 ? 8 : 4, columns = P == 2 ? 512 : 256;
@@ -402,8 +413,8 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
   __shared__ uint32_t tmem_base;
   __shared__ int failed_s;
   __shared__ float unit_s;
-  __shared__ float max_s[8 * G];
-  __shared__ __align__(16) float scale_s[BACK ? 8 * G : 1][32];
+  __shared__ float max_s[4 * G];
+  __shared__ __align__(16) float scale_s[BACK ? 4 * G : 1][64];
   __shared__ int32_t ids[256], runs[256], list[256];
   __shared__ uint32_t count_s, warp_sum[8], apart_s;
   volatile int* failed = &failed_s;
@@ -411,7 +422,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t rows_here = a.bt / P;  // rows of q that this CTA loads
   const uint32_t w_bytes = 8192 * KB, q_bytes = rows_here * 128 * KB, stage_bytes = w_bytes + q_bytes;
-  const uint32_t pair_base = base + a.stages * stage_bytes;  // P = 2: the adapters' operand, G of rows_here * 128 bytes
+  const uint32_t pair_base = base + a.stages * stage_bytes;  // P = 2: the adapters' operand, two of rows_here * 128 bytes
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
                  freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -425,10 +436,10 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 8 * (G < KB ? G : KB) + 1);  // the warps that read it and the matrix unit
+      mbar_init(empty + 8 * i, 4 * KB + 1);  // the warps that read it and the matrix unit
     }
     for (uint32_t i = 0; i < slots; ++i) {
-      mbar_init(ready + 8 * i, 8 * P);
+      mbar_init(ready + 8 * i, 4 * P);
       mbar_init(freed + 8 * i, 1);
     }
     mbar_init(done, 1);
@@ -464,11 +475,11 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
     if (lane == 0) {
       tma_prefetch(&map_w);
       tma_prefetch(&map_q);
-      uint32_t issued = 0;
+      uint32_t s = 0, turn = 0;  // stage, and the parity of its use
       bool ok = true;
       for (uint32_t i = 0; i < nb; ++i) {
-        const uint32_t s = i % a.stages, turn = i / a.stages;
-        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
+        // (a wait for the phase before the first passes at once)
+        if (!mbar_wait(empty + 8 * s, turn ^ 1, failed)) {
           ok = false;
           break;
         }
@@ -480,26 +491,20 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
 #pragma unroll
         for (int k = 0; k < KB; ++k)
           tma_load(at + w_bytes + k * rows_here * 128, &map_q, j + 64 * k, (int32_t)(t0 + side * rows_here), full + 8 * s);
-        ++issued;
+        if (++s == a.stages) s = 0, turn ^= 1;
       }
-      // a CTA does not end while its loads are in flight
-      if (!ok)
-        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
-          const long long start = clock64();
-          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
-          }
-        }
+      // a CTA does not end while its loads are in flight: the newest use of every stage
+      if (!ok) drain(full, s, turn, a.stages);
     }
   } else if (warp == 1) {
     if (lane == 0 && side == 0) {
       const uint32_t mask = 3u << leader;
       const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128 * P, a.bt);
-      uint32_t g = 0;  // 64-wide steps
+      uint32_t g = 0, s = 0, turn = 0;  // 64-wide steps, stage, parity
       bool ok = true;
       for (uint32_t i = 0; i < nb && ok; ++i) {
-        const uint32_t s = i % a.stages;
         // the other CTA's warps have waited for its tiles before they report a step ready
-        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+        ok = mbar_wait(full + 8 * s, turn, failed);
 #pragma unroll
         for (int k = 0; k < KB && ok; ++k, ++g) {
           const uint32_t slot = g % slots;
@@ -512,6 +517,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
           mma_commit<P>(freed + 8 * slot, mask);
         }
         if (ok) mma_commit<P>(empty + 8 * s, mask);
+        if (++s == a.stages) s = 0, turn ^= 1;
       }
       if (P == 2) {
         const uint32_t idesc_pair = idesc_f16(true, 128 * P, a.bt);
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
           ok = mbar_wait<true>(ready + 8 * slot, (g / slots) & 1, failed);
           if (!ok) break;
           fence_after();
-          const uint64_t b = desc_k128(pair_base + (g % G) * rows_here * 128);
+          const uint64_t b = desc_k128(pair_base + (i % 2) * rows_here * 128);
           const uint32_t first = (i * a.split + part) * 2;
           for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
             const uint32_t hi = tmem_a + slot * 32 + u * 16;
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
       if (ok) mma_commit<P>(done, mask);
     }
   } else {
-    const int w8 = warp - 2, quarter = warp % 4, half = w8 / 4 % 2, group = w8 / 8;
+    const int w4 = warp - 2, quarter = warp % 4, group = w4 / 4;
     const uint32_t row = quarter * 32 + lane;
     const uint64_t c = c0 + row;
     // with a scale for each term of the reduction the weights are scaled here, by powers of two that keep FP16 in range
@@ -542,14 +548,14 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
     float unit = 1.0f;
     if (scaled && !Widen<T>::kBf16) {
       float m = 0;
-      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += 256 * G) {
+      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += 128 * G) {
         const float s = fabsf(a.scale[i]);
         if (s <= 3e38f) m = fmaxf(m, s);
       }
       for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-      if (lane == 0) max_s[w8] = m;
-      asm volatile("bar.sync 1, %0;" ::"n"(256 * G) : "memory");
-      for (int i = 0; i < 8 * G; ++i) m = fmaxf(m, max_s[i]);
+      if (lane == 0) max_s[w4] = m;
+      asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");
+      for (int i = 0; i < 4 * G; ++i) m = fmaxf(m, max_s[i]);
       const uint32_t e = __float_as_uint(m) >> 23;  // unit = 2^-floor(log2 m), so that m * unit is in [1, 2)
       if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23);
       if (threadIdx.x == 64) unit_s = unit;
@@ -559,39 +565,39 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
     if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit : a.scale[c];
     const bool divides = fabsf(scale) >= 0x1p-40f && fabsf(scale) <= 0x1p40f;
 
-    // Group `group` of 8 warps takes every G-th 64-wide step.  A step's store is waited for, and announced, only when
-    // the next one has been widened, which hides its latency.
-    uint32_t pending = ~0u;
-    auto announce = [&] {
+    // Group `group` of 4 warps takes every G-th 64-wide step: a thread one row of the weights.
+    auto announce = [&](uint32_t slot) {
       wait_st();
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (P == 2 && side) mbar_arrive_at(ready + 8 * pending, leader);
-        else mbar_arrive(ready + 8 * pending);
+        if (P == 2 && side) mbar_arrive_at(ready + 8 * slot, leader);
+        else mbar_arrive(ready + 8 * slot);
       }
     };
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     bool ok = true;
-    uint32_t g = group;
+    uint32_t g = group, s = group / KB, turn = 0;
+    while (s >= a.stages) s -= a.stages, turn ^= 1;
     for (; g < steps; g += G) {
-      const uint32_t i = g / KB, k = g % KB, s = i % a.stages, at = base + s * stage_bytes;
-      const uint32_t slot = g % slots, turn = g / slots;
+      const uint32_t k = g % KB, at = base + s * stage_bytes, slot = g % slots;
       if (scaled) {
         // past the last term the scale is not read; the weights there are zeros
-        const uint64_t j = (uint64_t)b0 * 64 * KB + (uint64_t)g * 64 + half * 32 + lane;
-        const float v = j < a.n_scale ? a.scale[j] * unit : 0.0f;
+        const uint64_t j = (uint64_t)b0 * 64 * KB + (uint64_t)g * 64 + lane;
+        const float x = j < a.n_scale ? a.scale[j] * unit : 0.0f, y = j + 32 < a.n_scale ? a.scale[j + 32] * unit : 0.0f;
         __syncwarp();
-        scale_s[BACK ? w8 : 0][lane] = v;
+        scale_s[BACK ? w4 : 0][lane] = x;
+        scale_s[BACK ? w4 : 0][lane + 32] = y;
         __syncwarp();
       }
-      ok = __all_sync(~0u, mbar_wait(full + 8 * s, (i / a.stages) & 1, failed));
+      ok = mbar_wait_warp(full + 8 * s, turn, failed);
       if (!ok) break;
-      uint32_t v[16];
+      uint32_t v[32];
       if (!BACK) {
-        uint32_t b[8];
+        uint32_t b[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t chunk = k * 4 + half * 2 + h;
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t chunk = k * 4 + h;
           const uint32_t off = KB == 2 ? row * 128 + ((chunk ^ (row & 7)) << 4)
                                        : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
         if (Widen<T>::kBf16) {
           uint32_t bad = 0;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < 16; ++q) {
             uint32_t n0, n1;
             v[2 * q] = widen2_bf16(__byte_perm(b[q], 0, 0x4140), a.by, n0);
             v[2 * q + 1] = widen2_bf16(__byte_perm(b[q], 0, 0x4342), a.by, n1);
@@ -609,90 +615,94 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
           }
           if (bad & kNanTop)
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 16; ++q) {
               v[2 * q] = widen2_nan(__byte_perm(b[q], 0, 0x4140), v[2 * q]);
               v[2 * q + 1] = widen2_nan(__byte_perm(b[q], 0, 0x4342), v[2 * q + 1]);
             }
         } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
+          for (int q = 0; q < 16; ++q) {
             v[2 * q] = widen2_fp16(b[q]);
             v[2 * q + 1] = widen2_fp16(b[q] >> 16);
           }
         }
       } else {
-        const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
-        uint32_t b[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
-        if (Widen<T>::kBf16) {
-          uint32_t bad = 0;
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
+          uint32_t* w = v + 16 * half;
+          uint32_t b[32];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            uint32_t n;
-            v[j] = widen2_bf16(b[2 * j + 1] * 65536u + b[2 * j], a.by, n);
-            bad |= n;
+          for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
+          if (Widen<T>::kBf16) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              uint32_t n;
+              w[j] = widen2_bf16(b[2 * j + 1] * 65536u + b[2 * j], a.by, n);
+              bad |= n;
+            }
+            if (bad & kNanTop)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = widen2_nan(b[2 * j + 1] * 65536u + b[2 * j], w[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = widen2_fp16(b[2 * j + 1] * 256u + b[2 * j]);
           }
-          if (bad & kNanTop)
+          if (scaled)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = widen2_nan(b[2 * j + 1] * 65536u + b[2 * j], v[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = widen2_fp16(b[2 * j + 1] * 256u + b[2 * j]);
+            for (int j = 0; j < 16; j += 2) {
+              const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w4 : 0][32 * half + 2 * j]);
+              const float2 y = unpack<T>(w[j]), z = unpack<T>(w[j + 1]);
+              w[j] = Widen<T>::pack(y.x * x.x, y.y * x.y);
+              w[j + 1] = Widen<T>::pack(z.x * x.z, z.y * x.w);
+            }
         }
-        if (scaled)
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w8 : 0][2 * j]);
-            const float2 w = unpack<T>(v[j]), z = unpack<T>(v[j + 1]);
-            v[j] = Widen<T>::pack(w.x * x.x, w.y * x.y);
-            v[j + 1] = Widen<T>::pack(z.x * x.z, z.y * x.w);
-          }
       }
       __syncwarp();
-      if (lane == 0 && (G >= KB || k == KB - 1)) mbar_arrive(empty + 8 * s);
-      if (pending != ~0u) announce();
-      if (turn) {
-        ok = __all_sync(~0u, mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed));
-        if (!ok) break;
-        fence_after();
-      }
-      tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
-      pending = slot;
+      if (lane == 0) mbar_arrive(empty + 8 * s);
+      ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
+      if (!ok) break;
+      fence_after();
+      tmem_st32(tmem_a + slot * 32 + lanes, v);
+      announce(slot);
+      if (KB == 1 || G >= KB) s += G / KB;
+      else if (k == KB - 1) ++s;
+      if (s >= a.stages) s -= a.stages, turn ^= 1;
     }
-    if (ok && pending != ~0u) announce();
 
     if (P == 2) {
-      // Adapter steps: each half of a group widens one unit's factors; together they write the rows' side of both.
+      // Adapter steps: a thread widens two units' factors of its column, and writes its rows' side of both.
       const uint32_t chunks = (a.rank + 15) / 16;
       for (; g < steps + adapter_steps && ok; g += G) {
-        const uint32_t slot = g % slots, turn = g / slots, first = ((g - steps) * a.split + part) * 2;
-        // this slot is free; and so is the group's operand buffer, whose last reader was the step G before
-        if (turn) ok = __all_sync(~0u, mbar_wait(freed + 8 * slot, (turn - 1) & 1, failed));
-        if (ok && g >= steps + G)
-          ok = __all_sync(~0u, mbar_wait(freed + 8 * ((g - G) % slots), ((g - G) / slots) & 1, failed));
+        const uint32_t slot = g % slots, e = g - steps, first = (e * a.split + part) * 2;
+        // this slot is free, and so is the operand buffer, whose last reader was the step before the last
+        ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
+        if (ok && e >= 2) ok = mbar_wait_warp(freed + 8 * ((g - 2) % slots), (g - 2) / slots & 1, failed);
         if (!ok) break;
         fence_after();
-        uint32_t v[16] = {};
-        if (first + half < units) {
-          const int32_t id = list[(first + half) / chunks];
-          float f[16];
-          bool fits = c < a.cols && divides;
-          if (c < a.cols) fits = adapter_factor<T>(a, id, c, (first + half) % chunks * 16, a.alpha[id] / scale, f) && fits;
-          if (fits)
+        uint32_t v[32] = {};
 #pragma unroll
-            for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(f[2 * q], f[2 * q + 1], v[q], v[8 + q]);
-          else if (c < a.cols) apart_s = 0x3f800000u;
-        }
-        tmem_st16(tmem_a + slot * 32 + half * 16 + ((uint32_t)(quarter * 32) << 16), v);
-        const uint32_t to = pair_base + (g % G) * rows_here * 128;
-        for (uint32_t x = threadIdx.x - 64 - group * 256; x < rows_here * 2; x += 256) {
+        for (int u = 0; u < 2; ++u)
+          if (first + u < units) {
+            const int32_t id = list[(first + u) / chunks];
+            float f[16];
+            bool fits = c < a.cols && divides;
+            if (c < a.cols) fits = adapter_factor<T>(a, id, c, (first + u) % chunks * 16, a.alpha[id] / scale, f) && fits;
+            if (fits)
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                split_pair<__nv_bfloat16>(f[2 * q], f[2 * q + 1], v[16 * u + q], v[16 * u + 8 + q]);
+            else if (c < a.cols) apart_s = 0x3f800000u;
+          }
+        tmem_st32(tmem_a + slot * 32 + lanes, v);
+        const uint32_t to = pair_base + (e % 2) * rows_here * 128;
+        for (uint32_t x = threadIdx.x - 64 - group * 128; x < rows_here * 2; x += 128) {
           const uint32_t t = x / 2, u = x % 2;
-          const uint64_t tt = t0 + side * rows_here + t;
           uint32_t hi[8] = {}, lo[8] = {};
           if (first + u < units && ids[side * rows_here + t] == list[(first + u) / chunks]) {
             float y[16];
-            if (row_factor(a, tt, (first + u) % chunks * 16, y)) {
+            if (row_factor(a, t0 + side * rows_here + t, (first + u) % chunks * 16, y)) {
 #pragma unroll
               for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(y[2 * q], y[2 * q + 1], hi[q], lo[q]);
             } else {
@@ -708,21 +718,19 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
           }
         }
         fence_async();
-        pending = slot;
-        announce();
+        announce(slot);
       }
     }
-    ok = ok && mbar_wait(done, 0, failed);
-    ok = __all_sync(~0u, ok);
+    ok = ok && mbar_wait_warp(done, 0, failed);
     if (ok) fence_after();
-    if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(256 * G) : "memory");  // apart_s
+    if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");  // apart_s
 
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
     T* out = static_cast<T*>(a.out);
     if (a.split == 1) {
       const bool apart = P == 2 && apart_s;
       if (ok)
-        for (uint32_t t = (group * 2 + half) * 16; t < a.bt; t += 32 * G) {
+        for (uint32_t t = group * 16; t < a.bt; t += 16 * G) {
           if (t0 + t >= a.rows) break;
           float d[16];
           tmem_ld16(from + t, d);
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
         }
     } else if (ok) {
       // the tile's sums into this CTA's shared memory: every stage has been consumed
-      for (uint32_t t = (group * 2 + half) * 16; t < a.bt; t += 32 * G) {
+      for (uint32_t t = group * 16; t < a.bt; t += 16 * G) {
         float d[16];
         tmem_ld16(from + t, d);
 #pragma unroll
@@ -764,7 +772,7 @@ __global__ void __launch_bounds__(64 + 256 * G, P == 2 ? 1 : 2)
       bool apart = false;
       if (P == 2)
         for (uint32_t r = 0; r < a.split; ++r) apart |= cluster_ldf(smem_addr(&apart_s), r * P + side) != 0.0f;
-      for (uint32_t t = lo + n / 128; t < hi; t += 2 * G) {
+      for (uint32_t t = lo + n / 128; t < hi; t += G) {
         const uint64_t tt = t0 + t;
         if (tt >= a.rows || c >= a.cols) continue;
         float y = 0;
@@ -868,11 +876,10 @@ __global__ void __launch_bounds__(kShrinkThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t issued = 0;
+      uint32_t s = 0, turn = 0;  // stage, and the parity of its use
       bool ok = true;
       for (uint32_t i = 0; i < nb; ++i) {
-        const uint32_t s = i % a.stages, turn = i / a.stages;
-        if (turn && !mbar_wait(empty + 8 * s, (turn - 1) & 1, failed)) {
+        if (!mbar_wait(empty + 8 * s, turn ^ 1, failed)) {
           ok = false;
           break;
         }
@@ -882,29 +889,24 @@ __global__ void __launch_bounds__(kShrinkThreads)
         tma_load(at + f_bytes, &map_q, j, (int32_t)t0, full + 8 * s);
         for (uint32_t k = 0; k < mine; ++k)
           tma_load(at + k * pad * 128, &map_f, j, list[first + k] * (int32_t)a.rank, full + 8 * s);
-        ++issued;
+        if (++s == a.stages) s = 0, turn ^= 1;
       }
-      // a CTA does not end while its loads are in flight
-      if (!ok)
-        for (uint32_t i = issued > a.stages ? issued - a.stages : 0; i < issued; ++i) {
-          const long long start = clock64();
-          while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
-          }
-        }
+      if (!ok) drain(full, s, turn, a.stages);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, a.bt);
       bool ok = true;
+      uint32_t s = 0, turn = 0;
       for (uint32_t i = 0; i < nb && ok; ++i) {
-        const uint32_t s = i % a.stages;
-        ok = mbar_wait(full + 8 * s, (i / a.stages) & 1, failed);
+        ok = mbar_wait(full + 8 * s, turn, failed);
         if (!ok) break;
         fence_after();
         const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
 #pragma unroll
         for (int m = 0; m < 4; ++m) mma_ss(tmem, f + m * 2, q + m * 2, idesc, i > 0 || m > 0);
         mma_commit<1>(empty + 8 * s, 0);
+        if (++s == a.stages) s = 0, turn ^= 1;
       }
       if (ok) mma_commit<1>(done, 0);
     }
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int quarter = warp % 4, half = (warp - 2) / 4;
     const uint32_t row = quarter * 32 + lane;
     const uint32_t slot = row / pad, r = row % pad;
-    const bool ok = __all_sync(~0u, mbar_wait(done, 0, failed));
+    const bool ok = mbar_wait_warp(done, 0, failed);
     if (ok) {
       fence_after();
       const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
@@ -1100,7 +1102,7 @@ __global__ void __launch_bounds__(kOuterThreads)
             }
           }
         } else {
-          if (turn) ok = __all_sync(~0u, mbar_wait(empty + 8 * s, (turn - 1) & 1, failed));
+          if (turn) ok = mbar_wait_warp(empty + 8 * s, (turn - 1) & 1, failed);
           if (ok) {
             for (uint32_t x = threadIdx.x - 64; x < a.rank * 8; x += 256) {
               const uint32_t r = x % a.rank, t8 = x / a.rank;
@@ -1120,7 +1122,7 @@ __global__ void __launch_bounds__(kOuterThreads)
                            : "memory");
             }
             if (valid < 64) {
-              ok = __all_sync(~0u, mbar_wait(full + 8 * s, turn & 1, failed));
+              ok = mbar_wait_warp(full + 8 * s, turn & 1, failed);
               // whole 128-byte rows, so the swizzle does not matter
               for (uint32_t x = threadIdx.x - 64; x < (64 - valid) * 16; x += 256) {
                 const uint32_t to = at + (x / 8 % 2) * 8192 + (valid + x / 16) * 128 + x % 8 * 16;
@@ -1155,7 +1157,7 @@ __global__ void __launch_bounds__(kOuterThreads)
     const uint32_t row = quarter * 32 + lane;
     const uint64_t c = c0 + row;
     if (used) {
-      ok = __all_sync(~0u, ok && mbar_wait(done, 0, failed));
+      ok = ok && mbar_wait_warp(done, 0, failed);
       if (ok) fence_after();
     }
     if (ok)
@@ -1345,7 +1347,7 @@ int allow_smem(K kernel, bool (&set)[64]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ECF8_ERR_CUDA;
   if (dev < 64 && set[dev]) return ECF8_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess)
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 219 * 1024) != cudaSuccess)
     return ECF8_ERR_CUDA;
   if (dev < 64) set[dev] = true;
   return ECF8_OK;
@@ -1358,7 +1360,7 @@ int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductAr
   if (const int rc = allow_smem(product_tc<T, P, KB, G, BACK>, set)) return rc;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(64 + 256 * G);
+  cfg.blockDim = dim3(64 + 128 * G);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1381,7 +1383,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.len = len;
   a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
   const bool pair = a.bt > 128;  // two CTAs to a tile; else two CTAs to an SM
-  const int kb = pair ? 1 : 2, width = pair ? 2 : 1, groups = pair ? 2 : 1;
+  const int kb = pair ? 1 : 2, width = pair ? 2 : 1;
   a.blocks = (uint32_t)((len + 64 * kb - 1) / (64 * kb));
   const uint64_t tiles = (cols + 128 * width - 1) / (128 * width), row_tiles = (rows + a.bt - 1) / a.bt;
   if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
@@ -1390,7 +1392,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   const uint32_t most = 8 / width;
   a.split = 1;
   while (a.split < most && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
-  const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb, pairs = pair ? groups * here * 128 : 0;
+  const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb, pairs = pair ? 2 * here * 128 : 0;
   const uint32_t room = (pair ? 216 * 1024 - pairs : 106 * 1024) - 1024;
   a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
   size_t smem = (size_t)a.stages * stage + pairs + 1024;
@@ -1423,8 +1425,8 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
       make_map(&mq, type, in, len, rows, in_stride * 2, 64, here, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!made) return ECF8_ERR_CUDA;
   const dim3 grid((unsigned)(tiles * width * a.split), (unsigned)row_tiles);
-  return pair ? product_launch<T, 2, 1, 2, BACK>(mw, mq, a, grid, smem, s)
-              : product_launch<T, 1, 2, 1, BACK>(mw, mq, a, grid, smem, s);
+  return pair ? product_launch<T, 2, 1, 4, BACK>(mw, mq, a, grid, smem, s)
+              : product_launch<T, 1, 2, 2, BACK>(mw, mq, a, grid, smem, s);
 }
 
 // p = q f^T for every row's own adapter; f is n_adapters x rank rows of `len` values, f_stride apart.
@@ -1447,7 +1449,7 @@ int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint
   a.split = 1;
   while (a.split < 8 && chunks * row_tiles * a.split * 2 <= 148 && a.blocks / (a.split * 2) >= 4) a.split *= 2;
   const uint32_t stage = 16384 + a.bt * 128;
-  a.stages = (220 * 1024 - 1024) / stage < 8 ? (220 * 1024 - 1024) / stage : 8;
+  a.stages = (218 * 1024 - 1024) / stage < 8 ? (218 * 1024 - 1024) / stage : 8;
   size_t smem = (size_t)a.stages * stage + 1024;
   const size_t sums = (size_t)a.bt * 512 + 1024;
   if (a.split > 1 && smem < sums) smem = sums;
@@ -1502,7 +1504,7 @@ int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, u
   a.split = 1;
   while (a.split < 8 && tiles * n_adapters * a.split * 2 <= 148 && rows / (64 * a.split * 2) >= 2) a.split *= 2;
   const uint32_t pad = (rank + 7) / 8 * 8, stage = 16384 + pad * 256;
-  a.stages = (220 * 1024 - 1024) / stage < 8 ? (220 * 1024 - 1024) / stage : 8;
+  a.stages = (218 * 1024 - 1024) / stage < 8 ? (218 * 1024 - 1024) / stage : 8;
   const size_t smem = (size_t)a.stages * stage + 1024;  // at least the sums, pad * 512 bytes
   CUtensorMap mq;
   if (!make_map(&mq, Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, cols,

@@ -72,6 +72,13 @@ __device__ inline bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* fa
   }
 }
 
+// mbar_wait of a whole warp through one lane: 32 lanes that poll take turns (some 500 clocks a wait, measured).
+__device__ inline bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* failed) {
+  bool ok = true;
+  if (threadIdx.x % 32 == 0) ok = mbar_wait(bar, parity, failed);
+  return __all_sync(~0u, ok);
+}
+
 __device__ inline void tma_load(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
@@ -169,12 +176,14 @@ __host__ __device__ inline uint32_t idesc_f16(bool bf16, uint32_t m, uint32_t n)
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (n >> 3) << 17 | (m >> 4) << 24;
 }
 
-__device__ inline void tmem_st16(uint32_t tmem, const uint32_t (&v)[16]) {
+__device__ inline void tmem_st32(uint32_t tmem, const uint32_t (&v)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(tmem),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(tmem),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
 // The wait is part of the statement: nothing may read v between the two.
