@@ -171,18 +171,6 @@ __global__ void __launch_bounds__(256) product_simple(const T* q, uint64_t q_str
 // where they meet their own rows only and no rest; so are columns whose scale
 // is zero or extreme.
 
-// Two E4M3 bytes in bits 0-7 and 16-23 as a pair of T.  BF16: the sign to bit
-// 15, the magnitude to T's exponent and upper mantissa bits (subnormals come
-// out as T's), which is the value times 2^-120, and one exact product.  The
-// integer pipe and the multiply pipe both run at 64 lanes a clock (measured),
-// and all shifts on the first bound the widening; so the shifts are
-// multiplications, by factors that the compiler does not know (it would make
-// them shifts again).  FP16 has a conversion, 32 lanes a clock.
-struct WidenBy {
-  uint32_t magnitude;  // 16
-  uint32_t sign;       // 256
-  uint32_t one;        // 1
-};
 template <class T> struct Widen;
 template <> struct Widen<__nv_bfloat16> {
   static __device__ uint32_t pack(float a, float b) {
@@ -199,34 +187,30 @@ template <> struct Widen<__half> {
   static constexpr bool kBf16 = false;
 };
 
-// `top` gets a bit of kNanTop where a magnitude is 0x7f (NaN), which comes out as a finite value.
-constexpr uint32_t kNanTop = 0x08000800u;
-__device__ inline uint32_t widen2_bf16(uint32_t p, const WidenBy& by, uint32_t& top) {
-  const uint32_t m = (p * by.magnitude) & 0x07f007f0u;
-  top = m * by.one + 0x00100010u;
-  const uint32_t v = m | ((p * by.sign) & 0x80008000u), k = 0x7b807b80u;  // 2^120
-  const __nv_bfloat162 x =
-      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v), *reinterpret_cast<const __nv_bfloat162*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&x);
-}
-__device__ inline uint32_t widen2_nan(uint32_t p, uint32_t v) {
-  if ((p & 0x7f) == 0x7f) v = (v & 0xffff0000u) | 0x7fc0u;
-  if ((p & 0x7f0000) == 0x7f0000) v = (v & 0x0000ffffu) | 0x7fc00000u;
-  return v;
-}
-// Two E4M3 bytes next to each other as a pair of FP16.
-__device__ inline uint32_t widen2_fp16(uint32_t b) {
-  uint32_t v;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(v) : "r"(b));
-  return v;
-}
-
 template <class T> __device__ inline float2 unpack(uint32_t v);
 template <> __device__ inline float2 unpack<__nv_bfloat16>(uint32_t v) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 template <> __device__ inline float2 unpack<__half>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
+}
+
+// The two E4M3 bytes in bits 0-15 as a pair of FP16, as two float32, and as a
+// pair of T.  BF16 goes through float32: of the ways tried, the conversions
+// (185 clocks of an SM for 128 x 64 weights) beat moving the bits into BF16's
+// places and one product by 2^120 (291: integer and multiply pipes both run at
+// half rate, and NaN bytes need a check of their own).  FP16 takes 103.
+__device__ inline uint32_t widen2_fp16(uint32_t b) {
+  uint32_t v;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}" : "=r"(v) : "r"(b));
+  return v;
+}
+__device__ inline float2 widen2_float(uint32_t b) { return unpack<__half>(widen2_fp16(b)); }
+template <class T>
+__device__ inline uint32_t widen2(uint32_t b) {
+  if (!Widen<T>::kBf16) return widen2_fp16(b);
+  const float2 w = widen2_float(b);
+  return Widen<T>::pack(w.x, w.y);
 }
 
 // Two values as a pair of T and the pair of their rests.
@@ -307,7 +291,6 @@ struct ProductArgs {
   void* out;
   uint64_t out_stride;
   int32_t* status;
-  WidenBy by;
 };
 
 constexpr uint32_t kMaxStages = 16, kSlots = 8;
@@ -407,6 +390,7 @@ template <class T, int P, int KB, int G, int BACK>
 __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
                const __grid_constant__ ProductArgs a) {
+  // widened steps in tensor memory: as many as there are stages, which they then follow, or four
   constexpr uint32_t slots = P == 2 ? 8 : 4, columns = P == 2 ? 512 : 256;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
@@ -436,7 +420,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 4 * KB + 1);  // the warps that read it and the matrix unit
+      mbar_init(empty + 8 * i, 1);
     }
     for (uint32_t i = 0; i < slots; ++i) {
       mbar_init(ready + 8 * i, 4 * P);
@@ -478,11 +462,10 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       uint32_t s = 0, turn = 0;  // stage, and the parity of its use
       bool ok = true;
       for (uint32_t i = 0; i < nb; ++i) {
+        // a stage is free when its products have ended, and so have the warps that widened for them
         // (a wait for the phase before the first passes at once)
-        if (!mbar_wait(empty + 8 * s, turn ^ 1, failed)) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+        if (!ok) break;
         mbar_expect(full + 8 * s, stage_bytes);
         const uint32_t at = base + s * stage_bytes;
         const int32_t j = (int32_t)((b0 + i) * 64 * KB);
@@ -503,18 +486,17 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       uint32_t g = 0, s = 0, turn = 0;  // 64-wide steps, stage, parity
       bool ok = true;
       for (uint32_t i = 0; i < nb && ok; ++i) {
-        // the other CTA's warps have waited for its tiles before they report a step ready
-        ok = mbar_wait(full + 8 * s, turn, failed);
 #pragma unroll
         for (int k = 0; k < KB && ok; ++k, ++g) {
-          const uint32_t slot = g % slots;
-          ok = mbar_wait<P == 2>(ready + 8 * slot, (g / slots) & 1, failed);
+          // the warps that report a step ready have waited for their CTA's tiles
+          const uint32_t slot = P == 2 ? s : g % slots;
+          ok = mbar_wait<P == 2>(ready + 8 * slot, P == 2 ? turn : g / slots & 1, failed);
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * rows_here * 128);
 #pragma unroll
           for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
-          mma_commit<P>(freed + 8 * slot, mask);
+          if (P == 1) mma_commit<P>(freed + 8 * slot, mask);
         }
         if (ok) mma_commit<P>(empty + 8 * s, mask);
         if (++s == a.stages) s = 0, turn ^= 1;
@@ -522,19 +504,19 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (P == 2) {
         const uint32_t idesc_pair = idesc_f16(true, 128 * P, a.bt);
         for (uint32_t i = 0; i < adapter_steps && ok; ++i, ++g) {
-          const uint32_t slot = g % slots;
-          ok = mbar_wait<true>(ready + 8 * slot, (g / slots) & 1, failed);
+          ok = mbar_wait<true>(ready + 8 * s, turn, failed);
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(pair_base + (i % 2) * rows_here * 128);
           const uint32_t first = (i * a.split + part) * 2;
           for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
-            const uint32_t hi = tmem_a + slot * 32 + u * 16;
+            const uint32_t hi = tmem_a + s * 32 + u * 16;
             mma_ts<P>(tmem, hi, b + u * 4, idesc_pair, g > 0 || u > 0);
             mma_ts<P>(tmem, hi, b + u * 4 + 2, idesc_pair, 1);
             mma_ts<P>(tmem, hi + 8, b + u * 4, idesc_pair, 1);
           }
-          mma_commit<P>(freed + 8 * slot, mask);
+          mma_commit<P>(empty + 8 * s, mask);
+          if (++s == a.stages) s = 0, turn ^= 1;
         }
       }
       if (ok) mma_commit<P>(done, mask);
@@ -580,7 +562,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     uint32_t g = group, s = group / KB, turn = 0;
     while (s >= a.stages) s -= a.stages, turn ^= 1;
     for (; g < steps; g += G) {
-      const uint32_t k = g % KB, at = base + s * stage_bytes, slot = g % slots;
+      const uint32_t k = g % KB, at = base + s * stage_bytes, slot = P == 2 ? s : g % slots;
       if (scaled) {
         // past the last term the scale is not read; the weights there are zeros
         const uint64_t j = (uint64_t)b0 * 64 * KB + (uint64_t)g * 64 + lane;
@@ -604,27 +586,10 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
                        : "=r"(b[4 * h]), "=r"(b[4 * h + 1]), "=r"(b[4 * h + 2]), "=r"(b[4 * h + 3])
                        : "r"(at + off));
         }
-        if (Widen<T>::kBf16) {
-          uint32_t bad = 0;
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            uint32_t n0, n1;
-            v[2 * q] = widen2_bf16(__byte_perm(b[q], 0, 0x4140), a.by, n0);
-            v[2 * q + 1] = widen2_bf16(__byte_perm(b[q], 0, 0x4342), a.by, n1);
-            bad |= n0 | n1;
-          }
-          if (bad & kNanTop)
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              v[2 * q] = widen2_nan(__byte_perm(b[q], 0, 0x4140), v[2 * q]);
-              v[2 * q + 1] = widen2_nan(__byte_perm(b[q], 0, 0x4342), v[2 * q + 1]);
-            }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            v[2 * q] = widen2_fp16(b[q]);
-            v[2 * q + 1] = widen2_fp16(b[q] >> 16);
-          }
+        for (int q = 0; q < 16; ++q) {
+          v[2 * q] = widen2<T>(b[q]);
+          v[2 * q + 1] = widen2<T>(b[q] >> 16);
         }
       } else {
 #pragma unroll
@@ -634,34 +599,23 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           uint32_t b[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
-          if (Widen<T>::kBf16) {
-            uint32_t bad = 0;
+          if (!scaled) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint32_t n;
-              w[j] = widen2_bf16(b[2 * j + 1] * 65536u + b[2 * j], a.by, n);
-              bad |= n;
-            }
-            if (bad & kNanTop)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = widen2_nan(b[2 * j + 1] * 65536u + b[2 * j], w[j]);
+            for (int j = 0; j < 16; ++j) w[j] = widen2<T>(b[2 * j + 1] * 256u + b[2 * j]);
           } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = widen2_fp16(b[2 * j + 1] * 256u + b[2 * j]);
-          }
-          if (scaled)
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w4 : 0][32 * half + 2 * j]);
-              const float2 y = unpack<T>(w[j]), z = unpack<T>(w[j + 1]);
+              const float2 y = widen2_float(b[2 * j + 1] * 256u + b[2 * j]),
+                           z = widen2_float(b[2 * j + 3] * 256u + b[2 * j + 2]);
               w[j] = Widen<T>::pack(y.x * x.x, y.y * x.y);
               w[j + 1] = Widen<T>::pack(z.x * x.z, z.y * x.w);
             }
+          }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + 8 * s);
-      ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
+      // P = 2: the stage was loaded after its last products ended, and with them the slot's
+      if (P == 1) ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
       if (!ok) break;
       fence_after();
       tmem_st32(tmem_a + slot * 32 + lanes, v);
@@ -675,10 +629,11 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       // Adapter steps: a thread widens two units' factors of its column, and writes its rows' side of both.
       const uint32_t chunks = (a.rank + 15) / 16;
       for (; g < steps + adapter_steps && ok; g += G) {
-        const uint32_t slot = g % slots, e = g - steps, first = (e * a.split + part) * 2;
+        const uint32_t e = g - steps, first = (e * a.split + part) * 2;
         // this slot is free, and so is the operand buffer, whose last reader was the step before the last
-        ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
-        if (ok && e >= 2) ok = mbar_wait_warp(freed + 8 * ((g - 2) % slots), (g - 2) / slots & 1, failed);
+        ok = mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
+        if (ok && e >= 2)
+          ok = mbar_wait_warp(empty + 8 * (s >= 2 ? s - 2 : s + a.stages - 2), s >= 2 ? turn : turn ^ 1, failed);
         if (!ok) break;
         fence_after();
         uint32_t v[32] = {};
@@ -695,7 +650,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
                 split_pair<__nv_bfloat16>(f[2 * q], f[2 * q + 1], v[16 * u + q], v[16 * u + 8 + q]);
             else if (c < a.cols) apart_s = 0x3f800000u;
           }
-        tmem_st32(tmem_a + slot * 32 + lanes, v);
+        tmem_st32(tmem_a + s * 32 + lanes, v);
         const uint32_t to = pair_base + (e % 2) * rows_here * 128;
         for (uint32_t x = threadIdx.x - 64 - group * 128; x < rows_here * 2; x += 128) {
           const uint32_t t = x / 2, u = x % 2;
@@ -718,7 +673,9 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           }
         }
         fence_async();
-        announce(slot);
+        announce(s);
+        s += G;
+        if (s >= a.stages) s -= a.stages, turn ^= 1;
       }
     }
     ok = ok && mbar_wait_warp(done, 0, failed);
@@ -1394,7 +1351,8 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   while (a.split < most && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
   const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb, pairs = pair ? 2 * here * 128 : 0;
   const uint32_t room = (pair ? 216 * 1024 - pairs : 106 * 1024) - 1024;
-  a.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+  const uint32_t fit = room / stage, at_most = pair ? kSlots : kMaxStages;
+  a.stages = fit < at_most ? fit : at_most;
   size_t smem = (size_t)a.stages * stage + pairs + 1024;
   const size_t sums = (size_t)a.bt * 512 + 1024;
   if (a.split > 1 && smem < sums) smem = sums;
@@ -1413,7 +1371,6 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.out = out;
   a.out_stride = out_stride;
   a.status = d_status;
-  a.by = WidenBy{16, 256, 1};
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mw, mq;
