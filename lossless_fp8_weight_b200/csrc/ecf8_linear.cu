@@ -290,6 +290,7 @@ struct ProductArgs {
   uint32_t p_vector;     // and 4 of p
   void* out;
   uint64_t out_stride;
+  uint32_t out_vector;   // 4 columns of an output row are one aligned 8-byte store
   int32_t* status;
 };
 
@@ -718,28 +719,43 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   if (a.split > 1) {
     __syncwarp();
     cluster_sync();
-    // each CTA adds up and writes its share of the tile's rows
+    // each CTA adds up and writes its share of the tile's rows, a thread four columns at a time
     if (warp >= 2 && !*failed) {
-      const uint32_t n = threadIdx.x - 64, row = n % 128;
+      const uint32_t n = threadIdx.x - 64, row = n % 32 * 4;
       const uint64_t c = c0 + row;
       const uint32_t lo = a.bt * part / a.split, hi = a.bt * (part + 1) / a.split;
-      float scale = 1.0f;
-      if (c < a.cols) scale = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit_s : a.scale[c];
-      const bool divides = fabsf(scale) >= 0x1p-40f && fabsf(scale) <= 0x1p40f;
+      float scale[4];
+      bool divides[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        scale[k] = 1.0f;
+        if (c + k < a.cols)
+          scale[k] = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit_s : a.scale[c + k];
+        divides[k] = fabsf(scale[k]) >= 0x1p-40f && fabsf(scale[k]) <= 0x1p40f;
+      }
       bool apart = false;
       if (P == 2)
-        for (uint32_t r = 0; r < a.split; ++r) apart |= cluster_ldf(smem_addr(&apart_s), r * P + side) != 0.0f;
-      for (uint32_t t = lo + n / 128; t < hi; t += G) {
+        for (uint32_t r = 0; r < a.split; ++r) apart |= cluster_ldu(cluster_map(smem_addr(&apart_s), r * P + side)) != 0;
+      for (uint32_t t = lo + n / 32; t < hi; t += 4 * G) {
         const uint64_t tt = t0 + t;
         if (tt >= a.rows || c >= a.cols) continue;
-        float y = 0;
-        for (uint32_t r = 0; r < a.split; ++r) y += cluster_ldf(base + (t * 128 + row) * 4, r * P + side);
-        y *= scale;
-        if (a.rank && (P == 1 || apart)) {
-          const int32_t id = P == 1 ? a.row_id[tt] : ids[t];
-          if (id >= 0) y += P == 1 ? adapter_part<T>(a, id, tt, c, 0, a.rank) : left_out<T>(a, id, tt, c, scale, divides);
+        const float4 sum = cluster_sum4(base + (t * 128 + row) * 4, side, P, a.split);
+        float y[4] = {sum.x * scale[0], sum.y * scale[1], sum.z * scale[2], sum.w * scale[3]};
+        const int32_t id = a.rank && (P == 1 || apart) ? a.row_id[tt] : -1;
+        if (id >= 0)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < a.cols)
+              y[k] += P == 1 ? adapter_part<T>(a, id, tt, c + k, 0, a.rank)
+                             : left_out<T>(a, id, tt, c + k, scale[k], divides[k]);
+        T* out = static_cast<T*>(a.out) + tt * a.out_stride + c;
+        if (a.out_vector) {  // the columns are a multiple of 16
+          *reinterpret_cast<uint2*>(out) = make_uint2(Widen<T>::pack(y[0], y[1]), Widen<T>::pack(y[2], y[3]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < a.cols) put(out + k, y[k]);
         }
-        put(static_cast<T*>(a.out) + tt * a.out_stride + c, y);
       }
     }
   }
@@ -872,7 +888,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const uint32_t row = quarter * 32 + lane;
     const uint32_t slot = row / pad, r = row % pad;
     const bool ok = mbar_wait_warp(done, 0, failed);
-    if (ok) {
+    if (ok && quarter * 32 < mine * pad) {
       fence_after();
       const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
       for (uint32_t t = half * 16; t < a.bt; t += 32) {
@@ -891,14 +907,17 @@ __global__ void __launch_bounds__(kShrinkThreads)
     __syncwarp();
     cluster_sync();
     if (warp >= 2 && !*failed) {
-      const uint32_t k = threadIdx.x - 64, row = k % 128, slot = row / pad, r = row % pad;
-      const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
-      const uint32_t lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
-      for (uint32_t t = lo + k / 128; t < hi; t += 2) {
-        if (ids[t] != id) continue;
-        float d = 0;
-        for (uint32_t c = 0; c < a.split; ++c) d += cluster_ldf(base + (t * 128 + row) * 4, c);
-        a.p[(t0 + t) * a.rank + r] = d;
+      // a thread four ranks at a time (of one adapter: pad is a multiple of 8)
+      const uint32_t wide = mine * pad / 4, lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
+      for (uint32_t i = threadIdx.x - 64; i < (hi - lo) * wide; i += 256) {
+        const uint32_t t = lo + i / wide, row = i % wide * 4, slot = row / pad, r = row % pad;
+        if (ids[t] != list[first + slot]) continue;
+        const float4 d = cluster_sum4(base + (t * 128 + row) * 4, 0, 1, a.split);
+        float* p = a.p + (t0 + t) * a.rank + r;
+        if (r < a.rank) p[0] = d.x;
+        if (r + 1 < a.rank) p[1] = d.y;
+        if (r + 2 < a.rank) p[2] = d.z;
+        if (r + 3 < a.rank) p[3] = d.w;
       }
     }
     __syncwarp();
@@ -1148,13 +1167,15 @@ __global__ void __launch_bounds__(kOuterThreads)
     __syncwarp();
     cluster_sync();
     if (warp >= 2 && !*failed) {
-      const uint32_t k = threadIdx.x - 64, row = k % 128;
+      const uint32_t k = threadIdx.x - 64, row = k % 32 * 4;
       const uint64_t c = c0 + row;
       const uint32_t lo = a.rank * crank / a.split, hi = a.rank * (crank + 1) / a.split;
-      for (uint32_t r = lo + k / 128; r < hi; r += 2) {
-        float d = 0;
-        for (uint32_t q = 0; q < a.split; ++q) d += cluster_ldf(base + (r * 128 + row) * 4, q);
-        if (c < a.cols) put(out + r * a.sr + c * a.sc, d * alpha);
+      for (uint32_t r = lo + k / 32; r < hi; r += 8) {
+        const float4 d = cluster_sum4(base + (r * 128 + row) * 4, 0, 1, a.split);
+        const float y[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < a.cols) put(out + r * a.sr + (c + q) * a.sc, y[q] * alpha);
       }
     }
     __syncwarp();
@@ -1370,6 +1391,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.p_vector = l->rank % 4 == 0 && aligned(p, 16);
   a.out = out;
   a.out_stride = out_stride;
+  a.out_vector = aligned(out, 8) && out_stride % 4 == 0;
   a.status = d_status;
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;

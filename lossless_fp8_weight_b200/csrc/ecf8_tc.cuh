@@ -214,13 +214,34 @@ __device__ inline uint32_t cluster_rank() {
 __device__ inline void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ inline float cluster_ldf(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile("{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}"
-               : "=f"(v)
-               : "r"(addr), "r"(rank)
-               : "memory");
+// The address of a shared-memory location in another CTA of the cluster, and loads from it.  The loads are not
+// volatile, so that a thread has many in flight: they are for what does not change after a cluster_sync.
+__device__ inline uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ inline uint32_t cluster_ldu(uint32_t mapped) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapped) : "memory");
   return v;
+}
+// Adds up to 8 CTAs' four floats at this offset, ranks first, first + step, ..., in that order.
+__device__ inline float4 cluster_sum4(uint32_t addr, uint32_t first, uint32_t step, uint32_t count) {
+  float4 v[8];
+#pragma unroll
+  for (uint32_t r = 0; r < 8; ++r) {
+    v[r] = make_float4(0, 0, 0, 0);
+    if (r < count)
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                   : "r"(cluster_map(addr, first + r * step)));
+  }
+  float4 s = v[0];
+#pragma unroll
+  for (uint32_t r = 1; r < 8; ++r)
+    if (r < count) s.x += v[r].x, s.y += v[r].y, s.z += v[r].z, s.w += v[r].w;
+  return s;
 }
 __device__ inline void cluster_stu(uint32_t addr, uint32_t rank, uint32_t v) {
   asm volatile("{\n .reg .u32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.u32 [a], %2;\n}" ::"r"(addr),
