@@ -407,7 +407,6 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t rows_here = a.bt / P;  // rows of q that this CTA loads
   const uint32_t w_bytes = 8192 * KB, q_bytes = rows_here * 128 * KB, stage_bytes = w_bytes + q_bytes;
-  const uint32_t pair_base = base + a.stages * stage_bytes;  // P = 2: the adapters' operand, two of rows_here * 128 bytes
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
                  freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -457,31 +456,33 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   }
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch(&map_w);
       tma_prefetch(&map_q);
-      uint32_t s = 0, turn = 0;  // stage, and the parity of its use
-      bool ok = true;
-      for (uint32_t i = 0; i < nb; ++i) {
-        // a stage is free when its products have ended, and so have the warps that widened for them
-        // (a wait for the phase before the first passes at once)
-        ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
-        if (!ok) break;
-        mbar_expect(full + 8 * s, stage_bytes);
-        const uint32_t at = base + s * stage_bytes;
-        const int32_t j = (int32_t)((b0 + i) * 64 * KB);
-        if (BACK) tma_load(at, &map_w, (int32_t)c0, j, full + 8 * s);
-        else tma_load(at, &map_w, j, (int32_t)c0, full + 8 * s);
+    }
+    uint32_t s = 0, turn = 0;  // stage, and the parity of its use
+    bool ok = true;
+    for (uint32_t i = 0; i < nb; ++i) {
+      // a stage is free when its products have ended, and so have the warps that widened for them
+      // (a wait for the phase before the first passes at once)
+      ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+      if (!ok) break;
+      const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
+      const int32_t j = (int32_t)((b0 + i) * 64 * KB);
+      if (elect_one()) {
+        mbar_expect(bar, stage_bytes);
+        if (BACK) tma_load(at, &map_w, (int32_t)c0, j, bar);
+        else tma_load(at, &map_w, j, (int32_t)c0, bar);
 #pragma unroll
         for (int k = 0; k < KB; ++k)
-          tma_load(at + w_bytes + k * rows_here * 128, &map_q, j + 64 * k, (int32_t)(t0 + side * rows_here), full + 8 * s);
-        if (++s == a.stages) s = 0, turn ^= 1;
+          tma_load(at + w_bytes + k * rows_here * 128, &map_q, j + 64 * k, (int32_t)(t0 + side * rows_here), bar);
       }
-      // a CTA does not end while its loads are in flight: the newest use of every stage
-      if (!ok) drain(full, s, turn, a.stages);
+      __syncwarp();
+      if (++s == a.stages) s = 0, turn ^= 1;
     }
+    if (!ok) drain(full, s, turn, a.stages);
   } else if (warp == 1) {
-    if (lane == 0 && side == 0) {
+    if (side == 0) {
       const uint32_t mask = 3u << leader;
       const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128 * P, a.bt);
       uint32_t g = 0, s = 0, turn = 0;  // 64-wide steps, stage, parity
@@ -495,11 +496,14 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * rows_here * 128);
+          if (elect_one()) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
-          if (P == 1) mma_commit<P>(freed + 8 * slot, mask);
+            for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
+            if (P == 1) mma_commit<P>(freed + 8 * slot, mask);
+            if (k == KB - 1) mma_commit<P>(empty + 8 * s, mask);
+          }
+          __syncwarp();
         }
-        if (ok) mma_commit<P>(empty + 8 * s, mask);
         if (++s == a.stages) s = 0, turn ^= 1;
       }
       if (P == 2) {
@@ -508,19 +512,23 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           ok = mbar_wait<true>(ready + 8 * s, turn, failed);
           if (!ok) break;
           fence_after();
-          const uint64_t b = desc_k128(pair_base + (i % 2) * rows_here * 128);
+          const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes);
           const uint32_t first = (i * a.split + part) * 2;
-          for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
-            const uint32_t hi = tmem_a + s * 32 + u * 16;
-            mma_ts<P>(tmem, hi, b + u * 4, idesc_pair, g > 0 || u > 0);
-            mma_ts<P>(tmem, hi, b + u * 4 + 2, idesc_pair, 1);
-            mma_ts<P>(tmem, hi + 8, b + u * 4, idesc_pair, 1);
+          if (elect_one()) {
+            for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
+              const uint32_t hi = tmem_a + s * 32 + u * 16;
+              mma_ts<P>(tmem, hi, b + u * 4, idesc_pair, g > 0 || u > 0);
+              mma_ts<P>(tmem, hi, b + u * 4 + 2, idesc_pair, 1);
+              mma_ts<P>(tmem, hi + 8, b + u * 4, idesc_pair, 1);
+            }
+            mma_commit<P>(empty + 8 * s, mask);
           }
-          mma_commit<P>(empty + 8 * s, mask);
+          __syncwarp();
           if (++s == a.stages) s = 0, turn ^= 1;
         }
       }
-      if (ok) mma_commit<P>(done, mask);
+      if (ok && elect_one()) mma_commit<P>(done, mask);
+      __syncwarp();
     }
   } else {
     const int w4 = warp - 2, quarter = warp % 4, group = w4 / 4;
@@ -627,16 +635,11 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     }
 
     if (P == 2) {
-      // Adapter steps: a thread widens two units' factors of its column, and writes its rows' side of both.
+      // Adapter steps go on in the ring of stages: a thread widens two units' factors of its column into the slot, and
+      // writes its rows' side of both where the stage's rows were.  What they read is fetched before the wait.
       const uint32_t chunks = (a.rank + 15) / 16;
       for (; g < steps + adapter_steps && ok; g += G) {
-        const uint32_t e = g - steps, first = (e * a.split + part) * 2;
-        // this slot is free, and so is the operand buffer, whose last reader was the step before the last
-        ok = mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
-        if (ok && e >= 2)
-          ok = mbar_wait_warp(empty + 8 * (s >= 2 ? s - 2 : s + a.stages - 2), s >= 2 ? turn : turn ^ 1, failed);
-        if (!ok) break;
-        fence_after();
+        const uint32_t first = ((g - steps) * a.split + part) * 2;
         uint32_t v[32] = {};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -649,30 +652,38 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
 #pragma unroll
               for (int q = 0; q < 8; ++q)
                 split_pair<__nv_bfloat16>(f[2 * q], f[2 * q + 1], v[16 * u + q], v[16 * u + 8 + q]);
-            else if (c < a.cols) apart_s = 0x3f800000u;
+            else if (c < a.cols) apart_s = 1;
           }
-        tmem_st32(tmem_a + s * 32 + lanes, v);
-        const uint32_t to = pair_base + (e % 2) * rows_here * 128;
-        for (uint32_t x = threadIdx.x - 64 - group * 128; x < rows_here * 2; x += 128) {
+        const uint32_t to = base + s * stage_bytes + w_bytes;
+        bool waited = false;
+        for (uint32_t x = threadIdx.x - 64 - group * 128; x < (rows_here * 2 + 127) / 128 * 128; x += 128) {
           const uint32_t t = x / 2, u = x % 2;
           uint32_t hi[8] = {}, lo[8] = {};
-          if (first + u < units && ids[side * rows_here + t] == list[(first + u) / chunks]) {
+          if (t < rows_here && first + u < units && ids[side * rows_here + t] == list[(first + u) / chunks]) {
             float y[16];
             if (row_factor(a, t0 + side * rows_here + t, (first + u) % chunks * 16, y)) {
 #pragma unroll
               for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(y[2 * q], y[2 * q + 1], hi[q], lo[q]);
             } else {
-              for (uint32_t r = 0; r < 2; ++r) cluster_stu(smem_addr(&apart_s), leader + r, 0x3f800000u);
+              for (uint32_t r = 0; r < 2; ++r) cluster_stu(smem_addr(&apart_s), leader + r, 1);
             }
           }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t* z = q < 2 ? hi + 4 * q : lo + 4 * (q - 2);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + t * 128 + (((u * 4 + q) ^ (t & 7)) << 4)),
-                         "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3])
-                         : "memory");
+          if (!waited) {
+            ok = mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
+            waited = true;
           }
+          if (ok && t < rows_here)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t* z = q < 2 ? hi + 4 * q : lo + 4 * (q - 2);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + t * 128 + (((u * 4 + q) ^ (t & 7)) << 4)),
+                           "r"(z[0]), "r"(z[1]), "r"(z[2]), "r"(z[3])
+                           : "memory");
+            }
         }
+        if (!ok) break;
+        fence_after();
+        tmem_st32(tmem_a + s * 32 + lanes, v);
         fence_async();
         announce(s);
         s += G;
@@ -848,41 +859,44 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const uint32_t tmem = tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t s = 0, turn = 0;  // stage, and the parity of its use
-      bool ok = true;
-      for (uint32_t i = 0; i < nb; ++i) {
-        if (!mbar_wait(empty + 8 * s, turn ^ 1, failed)) {
-          ok = false;
-          break;
-        }
-        mbar_expect(full + 8 * s, q_bytes + mine * a.rank * 128);
-        const uint32_t at = base + s * stage_bytes;
-        const int32_t j = (int32_t)((b0 + i) * 64);
-        tma_load(at + f_bytes, &map_q, j, (int32_t)t0, full + 8 * s);
-        for (uint32_t k = 0; k < mine; ++k)
-          tma_load(at + k * pad * 128, &map_f, j, list[first + k] * (int32_t)a.rank, full + 8 * s);
-        if (++s == a.stages) s = 0, turn ^= 1;
+    uint32_t s = 0, turn = 0;  // stage, and the parity of its use
+    bool ok = true;
+    for (uint32_t i = 0; i < nb; ++i) {
+      ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+      if (!ok) break;
+      const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
+      const int32_t j = (int32_t)((b0 + i) * 64);
+      if (elect_one()) {
+        mbar_expect(bar, q_bytes + mine * a.rank * 128);
+        tma_load(at + f_bytes, &map_q, j, (int32_t)t0, bar);
       }
-      if (!ok) drain(full, s, turn, a.stages);
+      __syncwarp();
+      // the lanes share the adapters' loads
+      for (uint32_t k = lane; k < mine; k += 32)
+        tma_load(at + k * pad * 128, &map_f, j, list[first + k] * (int32_t)a.rank, bar);
+      __syncwarp();
+      if (++s == a.stages) s = 0, turn ^= 1;
     }
+    if (!ok) drain(full, s, turn, a.stages);
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, a.bt);
-      bool ok = true;
-      uint32_t s = 0, turn = 0;
-      for (uint32_t i = 0; i < nb && ok; ++i) {
-        ok = mbar_wait(full + 8 * s, turn, failed);
-        if (!ok) break;
-        fence_after();
-        const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
+    const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, a.bt);
+    bool ok = true;
+    uint32_t s = 0, turn = 0;
+    for (uint32_t i = 0; i < nb; ++i) {
+      ok = mbar_wait(full + 8 * s, turn, failed);
+      if (!ok) break;
+      fence_after();
+      const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
+      if (elect_one()) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) mma_ss(tmem, f + m * 2, q + m * 2, idesc, i > 0 || m > 0);
         mma_commit<1>(empty + 8 * s, 0);
-        if (++s == a.stages) s = 0, turn ^= 1;
       }
-      if (ok) mma_commit<1>(done, 0);
+      __syncwarp();
+      if (++s == a.stages) s = 0, turn ^= 1;
     }
+    if (ok && elect_one()) mma_commit<1>(done, 0);
+    __syncwarp();
   } else {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     const uint32_t row = quarter * 32 + lane;
@@ -1370,11 +1384,11 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   const uint32_t most = 8 / width;
   a.split = 1;
   while (a.split < most && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
-  const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb, pairs = pair ? 2 * here * 128 : 0;
-  const uint32_t room = (pair ? 216 * 1024 - pairs : 106 * 1024) - 1024;
+  const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb;
+  const uint32_t room = (pair ? 216 * 1024 : 106 * 1024) - 1024;
   const uint32_t fit = room / stage, at_most = pair ? kSlots : kMaxStages;
   a.stages = fit < at_most ? fit : at_most;
-  size_t smem = (size_t)a.stages * stage + pairs + 1024;
+  size_t smem = (size_t)a.stages * stage + 1024;
   const size_t sums = (size_t)a.bt * 512 + 1024;
   if (a.split > 1 && smem < sums) smem = sums;
   a.scale = l->d_scale;
