@@ -539,17 +539,20 @@ def _dtype_of(t, what: str) -> int:
     return d
 
 
-def _is(t, what: str, dtype: str, shape) -> None:
+def _is(t, what: str, dtype, shape) -> None:
     """A contiguous tensor of this type and shape."""
-    if str(t.dtype) != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         _refuse(what, f"want a contiguous {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
-def _rows(t, what: str, dtype: str, rows: int, cols: int) -> int:
+def _rows(t, what: str, dtype, rows: int, cols: int) -> int:
     """The row stride of a rows x cols tensor whose rows are contiguous."""
-    if str(t.dtype) != dtype or tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
-        _refuse(what, f"want {dtype} of shape {(rows, cols)} with contiguous rows, got {t.dtype} {tuple(t.shape)}")
-    return max(t.stride(0), cols) if rows <= 1 else t.stride(0)
+    if t.dtype is not dtype or t.shape != (rows, cols):
+        _refuse(what, f"want {dtype} of shape {(rows, cols)}, got {t.dtype} {tuple(t.shape)}")
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        _refuse(what, f"rows of {cols} values have to be contiguous, got a stride of {inner}")
+    return stride if rows > 1 else max(stride, cols)
 
 
 @dataclass
@@ -617,7 +620,7 @@ class Linear:
             n, k = weight.shape
             if weight.element_size() != 1:
                 _refuse("Linear", f"weights are E4M3 bytes, got {weight.dtype}")
-            d.w_stride = _rows(weight, "Linear weight", str(weight.dtype), n, k)
+            d.w_stride = _rows(weight, "Linear weight", weight.dtype, n, k)
         d.d_w, d.n_out, d.k_in, d.dtype = _ptr(weight), n, k, _DTYPES[str(dtype)]
         if scale is not None:
             if str(scale.dtype) != "torch.float32" or scale.numel() not in (1, n) or not scale.is_contiguous():
@@ -626,13 +629,14 @@ class Linear:
         self.rank = 0
         if adapters is not None and adapters.a.shape[0]:
             count, self.rank = (int(v) for v in adapters.a.shape[:2])
-            _is(adapters.a, "Linear adapters a", str(dtype), (count, self.rank, k))
-            _is(adapters.b, "Linear adapters b", str(dtype), (count, n, self.rank))
-            _is(adapters.alpha, "Linear adapters alpha", "torch.float32", (count,))
+            _is(adapters.a, "Linear adapters a", dtype, (count, self.rank, k))
+            _is(adapters.b, "Linear adapters b", dtype, (count, n, self.rank))
+            _is(adapters.alpha, "Linear adapters alpha", torch.float32, (count,))
             d.d_a, d.d_b, d.d_alpha = _ptr(adapters.a), _ptr(adapters.b), _ptr(adapters.alpha)
             d.n_adapters, d.rank = count, self.rank
         self.n_out, self.k_in, self.dtype = int(n), int(k), dtype
-        self._name, self._keep, self._d, self._ref = str(dtype), (weight, scale, adapters), d, ctypes.byref(d)
+        self._keep, self._d, self._ref = (weight, scale, adapters), d, ctypes.byref(d)
+        self._f32, self._i32 = torch.float32, torch.int32
 
     def workspace_size(self, rows: int) -> int:
         """Bytes of device workspace forward and backward need for this many rows."""
@@ -641,19 +645,21 @@ class Linear:
     def _requests(self, q):
         if q is None:
             return None
-        _is(q.ids, "Requests ids", "torch.int32", (q.ids.numel(),))
-        _is(q.offsets, "Requests offsets", "torch.int32", (q.ids.numel() + 1,))
-        return RequestsDesc(_ptr(q.offsets), _ptr(q.ids), q.ids.numel())
+        ids, offsets = q.ids, q.offsets
+        count = ids.numel()
+        _is(ids, "Requests ids", self._i32, (count,))
+        _is(offsets, "Requests offsets", self._i32, (count + 1,))
+        return RequestsDesc(offsets.data_ptr(), ids.data_ptr(), count)
 
     def forward(self, x, y, requests: Optional[Requests] = None, u=None, workspace=None, status=None,
                 stream=None) -> None:
         """Asynchronously writes y (rows, out) for x (rows, in).  ``u`` (rows,
         rank) float32 keeps A x for ``backward``."""
         rows = x.shape[0]
-        xs = _rows(x, "Linear x", self._name, rows, self.k_in)
-        ys = _rows(y, "Linear y", self._name, rows, self.n_out)
+        xs = _rows(x, "Linear x", self.dtype, rows, self.k_in)
+        ys = _rows(y, "Linear y", self.dtype, rows, self.n_out)
         if u is not None:
-            _is(u, "Linear u", "torch.float32", (rows, self.rank))
+            _is(u, "Linear u", self._f32, (rows, self.rank))
         _check(_lib.ecf8_linear_forward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(y), ys, rows, _ptr(u),
                                         _ptr(workspace), _nbytes(workspace, 0), _ptr(status), _stream(stream)),
                "ecf8_linear_forward")
@@ -664,16 +670,16 @@ class Linear:
         (rows, in), da and db (as the adapters' a and b), from dy (rows, out),
         the forward pass's x (for da) and u (for db)."""
         rows = dy.shape[0]
-        ds = _rows(dy, "Linear dy", self._name, rows, self.n_out)
-        xs = _rows(x, "Linear x", self._name, rows, self.k_in) if x is not None else self.k_in
-        gs = _rows(dx, "Linear dx", self._name, rows, self.k_in) if dx is not None else self.k_in
+        ds = _rows(dy, "Linear dy", self.dtype, rows, self.n_out)
+        xs = _rows(x, "Linear x", self.dtype, rows, self.k_in) if x is not None else self.k_in
+        gs = _rows(dx, "Linear dx", self.dtype, rows, self.k_in) if dx is not None else self.k_in
         if u is not None:
-            _is(u, "Linear u", "torch.float32", (rows, self.rank))
+            _is(u, "Linear u", self._f32, (rows, self.rank))
         for g, of, what in ((da, "a", "Linear da"), (db, "b", "Linear db")):
             if g is not None:
                 if not self.rank:
                     _refuse(what, "there are no adapters")
-                _is(g, what, self._name, getattr(self._keep[2], of).shape)
+                _is(g, what, self.dtype, getattr(self._keep[2], of).shape)
         _check(_lib.ecf8_linear_backward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(dy), ds, _ptr(u),
                                          _ptr(dx), gs, _ptr(da), _ptr(db), rows, _ptr(workspace),
                                          _nbytes(workspace, 0), _ptr(status), _stream(stream)),

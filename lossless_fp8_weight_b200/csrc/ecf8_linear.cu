@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     // the other CTA's barriers are ready before anything arrives on them
     cluster_sync();
     if (a.rank) {
+      wait_predecessor();
       if (threadIdx.x < 256) ids[threadIdx.x] = threadIdx.x < a.bt && t0 + threadIdx.x < a.rows ? a.row_id[t0 + threadIdx.x] : -1;
       __syncthreads();
       distinct(ids, a.bt, runs, list, &count_s, warp_sum);
@@ -692,6 +693,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     }
     ok = ok && mbar_wait_warp(done, 0, failed);
     if (ok) fence_after();
+    wait_predecessor();  // row_id and p are there, and nothing before this call reads the output any more
     if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");  // apart_s
 
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -797,7 +799,10 @@ struct ShrinkArgs {
   uint32_t blocks;       // 64-wide steps of the reduction
   uint32_t bt, stages, split;
   uint32_t rank, per;    // ranks of an adapter, adapters in a chunk of 128 lanes
-  const int32_t* row_id;
+  const int32_t* offsets;
+  const int32_t* request_ids;
+  uint32_t count, n_adapters;
+  int32_t* row_id;       // written: the adapter of every row, -1 for none
   float* p;              // rows x rank
   int32_t* status;
 };
@@ -829,7 +834,8 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const uint32_t pad = (a.rank + 7) / 8 * 8;
 
   const uint32_t n = (uint32_t)(a.rows - t0 < a.bt ? a.rows - t0 : a.bt);
-  if (threadIdx.x < 256) ids[threadIdx.x] = threadIdx.x < n ? a.row_id[t0 + threadIdx.x] : -1;
+  start_successor();
+  if (threadIdx.x < 256) ids[threadIdx.x] = -1;
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
       mbar_init(full + 8 * i, 1);
@@ -840,6 +846,19 @@ __global__ void __launch_bounds__(kShrinkThreads)
     mbar_init_fence();
   }
   __syncthreads();
+  // the requests that reach into this tile write their rows' ids
+  for (uint32_t i = threadIdx.x; i < a.count; i += kShrinkThreads) {
+    const int32_t b = a.offsets[i], e = a.offsets[i + 1], id = a.request_ids[i];
+    const bool known = id < 0 || (uint32_t)id < a.n_adapters;
+    if (b < 0 || e < b || (int64_t)e > (int64_t)a.rows || !known) {
+      if (a.status && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, ECF8_STATUS_BAD_REQUEST);
+    }
+    if (id < 0 || !known) continue;
+    const int64_t lo = max((int64_t)b - (int64_t)t0, (int64_t)0), hi = min((int64_t)e - (int64_t)t0, (int64_t)n);
+    for (int64_t t = lo; t < hi; ++t) ids[t] = id;
+  }
+  __syncthreads();
+  if (chunk == 0 && crank == 0 && threadIdx.x < n) a.row_id[t0 + threadIdx.x] = ids[threadIdx.x];
   distinct(ids, n, runs, list, &count_s, warp_sum);
   // rows without an adapter have zeros
   if (chunk == 0 && crank == 0)
@@ -1347,7 +1366,7 @@ int allow_smem(K kernel, bool (&set)[64]) {
 
 template <class T, int P, int KB, int G, int BACK>
 int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductArgs& a, dim3 grid, size_t smem,
-                   cudaStream_t s) {
+                   bool overlap, cudaStream_t s) {
   static bool set[64] = {};
   if (const int rc = allow_smem(product_tc<T, P, KB, G, BACK>, set)) return rc;
   cudaLaunchConfig_t cfg{};
@@ -1355,19 +1374,21 @@ int product_launch(const CUtensorMap& mw, const CUtensorMap& mq, const ProductAr
   cfg.blockDim = dim3(64 + 128 * G);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = P * a.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = overlap ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, product_tc<T, P, KB, G, BACK>, mw, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
 template <class T, int BACK>
 int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out,
-                   uint64_t out_stride, uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status,
-                   cudaStream_t s) {
+                   uint64_t out_stride, uint64_t rows, const int32_t* row_id, const float* p, bool overlap,
+                   int32_t* d_status, cudaStream_t s) {
   const uint64_t cols = BACK ? l->k_in : l->n_out, len = BACK ? l->n_out : l->k_in;
   ProductArgs a{};
   a.rows = rows;
@@ -1418,34 +1439,45 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
       make_map(&mq, type, in, len, rows, in_stride * 2, 64, here, CU_TENSOR_MAP_SWIZZLE_128B);
   if (!made) return ECF8_ERR_CUDA;
   const dim3 grid((unsigned)(tiles * width * a.split), (unsigned)row_tiles);
-  return pair ? product_launch<T, 2, 1, 4, BACK>(mw, mq, a, grid, smem, s)
-              : product_launch<T, 1, 2, 2, BACK>(mw, mq, a, grid, smem, s);
+  return pair ? product_launch<T, 2, 1, 4, BACK>(mw, mq, a, grid, smem, overlap, s)
+              : product_launch<T, 1, 2, 2, BACK>(mw, mq, a, grid, smem, overlap, s);
 }
 
 // p = q f^T for every row's own adapter; f is n_adapters x rank rows of `len` values, f_stride apart.
 template <class T>
 int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint64_t f_stride, uint64_t len,
-                  uint32_t n_adapters, uint32_t rank, const int32_t* row_id, float* p, int32_t* d_status,
-                  cudaStream_t s) {
+                  uint32_t n_adapters, uint32_t rank, const ecf8_requests* req, int32_t* row_id, float* p,
+                  int32_t* d_status, cudaStream_t s) {
   static bool set[64] = {};
   if (const int rc = allow_smem(shrink_tc<T>, set)) return rc;
   ShrinkArgs a{};
   a.rows = rows;
   a.blocks = (uint32_t)((len + 63) / 64);
-  a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
   a.rank = rank;
   a.per = 128 / ((rank + 7) / 8 * 8);
-  const uint64_t most = n_adapters < a.bt ? n_adapters : a.bt, chunks = (most + a.per - 1) / a.per,
-                 row_tiles = (rows + a.bt - 1) / a.bt;
+  // The largest tiles (q's rows against the adapters' are what is read again) that still give every SM a CTA once
+  // the reduction is split, which leaves a CTA two steps at least.
+  uint64_t chunks, row_tiles;
+  for (a.bt = 256;; a.bt /= 2) {
+    const uint64_t most = n_adapters < a.bt ? n_adapters : a.bt;
+    chunks = (most + a.per - 1) / a.per;
+    row_tiles = (rows + a.bt - 1) / a.bt;
+    a.split = 1;
+    while (a.split < 8 && chunks * row_tiles * a.split * 2 <= 148 && a.blocks / (a.split * 2) >= 2) a.split *= 2;
+    if (a.bt == 32 || chunks * row_tiles * a.split > 74) break;
+  }
+  if (rows < a.bt) a.bt = (uint32_t)((rows + 15) / 16 * 16);
   if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
-  // a CTA to every SM, but at least four steps to a CTA
-  a.split = 1;
-  while (a.split < 8 && chunks * row_tiles * a.split * 2 <= 148 && a.blocks / (a.split * 2) >= 4) a.split *= 2;
   const uint32_t stage = 16384 + a.bt * 128;
-  a.stages = (218 * 1024 - 1024) / stage < 8 ? (218 * 1024 - 1024) / stage : 8;
+  // small tiles leave room for a CTA of the projection beside them
+  a.stages = a.bt <= 64 ? 4 : 216 * 1024 / stage < 8 ? 216 * 1024 / stage : 8;
   size_t smem = (size_t)a.stages * stage + 1024;
   const size_t sums = (size_t)a.bt * 512 + 1024;
   if (a.split > 1 && smem < sums) smem = sums;
+  a.offsets = req->d_offsets;
+  a.request_ids = req->d_ids;
+  a.count = req->count;
+  a.n_adapters = n_adapters;
   a.row_id = row_id;
   a.p = p;
   a.status = d_status;
@@ -1519,9 +1551,9 @@ int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, u
 
 template <class T, int BACK>
 int product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
-            uint64_t rows, const int32_t* row_id, const float* p, int32_t* d_status, cudaStream_t s) {
+            uint64_t rows, const int32_t* row_id, const float* p, bool overlap, int32_t* d_status, cudaStream_t s) {
   if (tensor_path(l, in, in_stride))
-    return product_tensor<T, BACK>(l, adapted, in, in_stride, out, out_stride, rows, row_id, p, d_status, s);
+    return product_tensor<T, BACK>(l, adapted, in, in_stride, out, out_stride, rows, row_id, p, overlap, d_status, s);
   const uint64_t cols = BACK ? l->k_in : l->n_out, len = BACK ? l->n_out : l->k_in;
   const uint64_t step = kGridY * 64;
   for (uint64_t t = 0; t < rows; t += step) {
@@ -1542,14 +1574,16 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   const Plan w = plan_of(l, rows);
   int32_t* row_id = reinterpret_cast<int32_t*>(ws);
   const bool keep = u != nullptr;
+  bool overlap = false;  // the projection may start beside the kernel before it
   if (l->n_adapters && !u) u = reinterpret_cast<float*>(ws + w.p);
   if (adapted) {
-    route(l, q, rows, row_id, d_status, s);
     if (tensor_path(l, x, x_stride) && aligned(l->d_a, 16)) {
       const int rc = shrink_tensor<T>(static_cast<const T*>(x), x_stride, rows, static_cast<const T*>(l->d_a), l->k_in,
-                                      l->k_in, l->n_adapters, l->rank, row_id, u, d_status, s);
+                                      l->k_in, l->n_adapters, l->rank, q, row_id, u, d_status, s);
       if (rc) return rc;
+      overlap = true;
     } else {
+      route(l, q, rows, row_id, d_status, s);
       shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
           static_cast<const T*>(x), x_stride, static_cast<const T*>(l->d_a), l->rank * l->k_in, l->k_in, 1, l->k_in,
           l->rank, row_id, u);
@@ -1557,7 +1591,7 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   } else if (l->n_adapters && keep) {
     if (cudaMemsetAsync(u, 0, rows * l->rank * 4, s) != cudaSuccess) return ECF8_ERR_CUDA;
   }
-  const int rc = product<T, 0>(l, adapted, x, x_stride, y, y_stride, rows, row_id, u, d_status, s);
+  const int rc = product<T, 0>(l, adapted, x, x_stride, y, y_stride, rows, row_id, u, overlap, d_status, s);
   if (rc) return rc;
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
@@ -1570,23 +1604,27 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   const Plan w = plan_of(l, rows);
   int32_t* row_id = reinterpret_cast<int32_t*>(ws);
   float* v = reinterpret_cast<float*>(ws + w.p);
-  if (adapted) route(l, q, rows, row_id, d_status, s);
+  bool overlap = false;
   if (adapted && (dx || da)) {
     if (tensor_path(l, dy, dy_stride)) {
       T* turned = reinterpret_cast<T*>(ws + w.turned);
       transpose_kernel<T><<<dim3((unsigned)((l->n_out + 63) / 64), l->n_adapters), 256, 0, s>>>(
           static_cast<const T*>(l->d_b), turned, l->n_out, l->n_out, l->rank);
       const int rc = shrink_tensor<T>(static_cast<const T*>(dy), dy_stride, rows, turned, l->n_out, l->n_out,
-                                      l->n_adapters, l->rank, row_id, v, d_status, s);
+                                      l->n_adapters, l->rank, q, row_id, v, d_status, s);
       if (rc) return rc;
+      overlap = true;
     } else {
+      route(l, q, rows, row_id, d_status, s);
       shrink_simple<T><<<dim3((unsigned)rows, (l->rank + 7) / 8), 128, 0, s>>>(
           static_cast<const T*>(dy), dy_stride, static_cast<const T*>(l->d_b), l->n_out * l->rank, 1, l->rank,
           l->n_out, l->rank, row_id, v);
     }
+  } else if (adapted) {
+    route(l, q, rows, row_id, d_status, s);
   }
   if (dx && rows) {
-    const int rc = product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, d_status, s);
+    const int rc = product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, overlap, d_status, s);
     if (rc) return rc;
   }
   const uint32_t count = adapted ? q->count : 0;

@@ -215,6 +215,11 @@ __device__ inline void tmem_ld8(uint32_t tmem, float (&v)[8]) {
       : "memory");
 }
 
+// A kernel launched to overlap its predecessor waits for that one's end and results with the first; the predecessor
+// lets it start with the second.
+__device__ inline void wait_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ inline void start_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ inline uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
