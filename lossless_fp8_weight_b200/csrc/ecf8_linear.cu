@@ -582,7 +582,10 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         scale_s[BACK ? w4 : 0][lane + 32] = y;
         __syncwarp();
       }
-      ok = mbar_wait_warp(full + 8 * s, turn, failed);
+      // A group skips the stage's uses by the others, and a barrier tells its phases apart by their parity alone: the
+      // stage's last products have ended (which no phase can overtake, as this step is still to come), then its
+      // load is the one waited for.
+      ok = (P == 1 || mbar_wait_warp(empty + 8 * s, turn ^ 1, failed)) && mbar_wait_warp(full + 8 * s, turn, failed);
       if (!ok) break;
       uint32_t v[32];
       if (!BACK) {
@@ -984,35 +987,53 @@ __global__ void __launch_bounds__(256) transpose_kernel(const T* in, T* out, uin
 //     D[c][r] = sum over the adapter's rows of q[t][c] p[t][r]
 //
 // Bound: one read of q (x for da, dy for db).  A CTA takes one adapter and 128
-// columns; q's tiles are read as TMA left them, the reduction running across
-// their rows.  p is float32 and is split into a 16-bit part and a 16-bit
-// rest, side by side as columns (2^-17 of a value is lost in BF16, 2^-22 in
-// FP16), so the rest costs columns, not another pass.  FP16 parts are taken of
-// p times a power of two that brings the adapter's largest to 2^14.  Blocks are
-// 64 rows of one request; rows past its end are cleared, since the next
-// request's may hold infinities.  Few columns split the blocks over a cluster.
+// columns of da or of db; tiles of 64 rows are read as TMA left them, the
+// reduction running across their rows.  p is float32 and has been split into a
+// 16-bit part and a 16-bit rest, side by side as columns (2^-17 of a value is
+// lost in BF16, 2^-22 in FP16), so the rest costs columns, not another pass.
+// (Splitting it here, tile by tile, made the split the bound: 384 us for 8192
+// rows of 8192 at rank 64.)  Blocks are 64 rows of one request; rows past its
+// end are cleared in shared memory, since the next request's may hold
+// infinities.  Few columns split the blocks over a cluster.  A CTA uses half of
+// an SM's shared and tensor memory, so that two hide each other's ends.
 
+struct OuterSide {
+  uint64_t cols;
+  uint32_t tiles;
+  const uint32_t* peak;  // FP16: bits of the largest |p| of each adapter
+  void* out;
+  uint64_t sr, sc;       // element (r, c) of an adapter at r * sr + c * sc
+  uint32_t out_vector;   // 8 ranks of a column are one aligned 16-byte store
+};
 struct OuterArgs {
-  uint64_t rows, cols;
+  uint64_t rows;
   uint32_t stages, split, rank;
-  const float* p;
   const int32_t* offsets;
   const int32_t* ids;
   uint32_t count;
-  const uint32_t* peak;  // FP16: bits of the largest |p| of each adapter
   const float* alpha;
-  void* out;
-  uint64_t f_adapter, sr, sc;
-  uint32_t out_vector;   // 8 ranks of a column are one aligned 16-byte store
+  OuterSide side[2];
   int32_t* status;
 };
 
 constexpr int kOuterThreads = 320;
 constexpr uint32_t kWindow = 320;  // requests looked through at a time
 
+__host__ __device__ inline uint32_t padded(uint32_t rank) { return (rank + 7) / 8 * 8; }
+// Columns of p's parts: the 16-bit values, their rests, and zeros up to whole boxes of 64.
+__host__ __device__ inline uint32_t part_columns(uint32_t rank) { return (2 * padded(rank) + 63) / 64 * 64; }
+
+// The power of two by which FP16 parts of p are taken: it brings the largest to [2^13, 2^14).
+__device__ inline float unit_of(uint32_t peak) {
+  const uint32_t e = peak >> 23;  // the largest is in [2^(e-127), 2^(e-126))
+  return __uint_as_float((e > 14 ? 267 - e : 253) << 23);
+}
+
 template <class T>
-__global__ void __launch_bounds__(kOuterThreads)
-    outer_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ OuterArgs a) {
+__global__ void __launch_bounds__(kOuterThreads, 2)
+    outer_tc(const __grid_constant__ CUtensorMap map_q0, const __grid_constant__ CUtensorMap map_p0,
+             const __grid_constant__ CUtensorMap map_q1, const __grid_constant__ CUtensorMap map_p1,
+             const __grid_constant__ OuterArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 1];
   __shared__ uint32_t tmem_base;
@@ -1021,22 +1042,26 @@ __global__ void __launch_bounds__(kOuterThreads)
   __shared__ uint32_t warp_sum[kOuterThreads / 32];
   volatile int* failed = &failed_s;
 
-  const uint32_t pad = (a.rank + 7) / 8 * 8, n = 2 * pad;
+  const uint32_t pad = padded(a.rank), n = part_columns(a.rank);
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_bytes = 16384, stage_bytes = q_bytes + n * 128;
-  const uint32_t full = smem_addr(bars), ready = full + 8 * kMaxStages, empty = ready + 8 * kMaxStages,
-                 done = empty + 8 * kMaxStages;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
+                 done = ready + 8 * kMaxStages;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
-  const uint64_t c0 = (uint64_t)(blockIdx.x / a.split) * 128;
+  const uint32_t tile = blockIdx.x / a.split, which = tile < a.side[0].tiles ? 0 : 1;
+  const OuterSide& side = a.side[which];
+  const CUtensorMap* map_q = which ? &map_q1 : &map_q0;
+  const CUtensorMap* map_p = which ? &map_p1 : &map_p0;
+  const uint64_t c0 = (uint64_t)(which ? tile - a.side[0].tiles : tile) * 128;
   const int32_t id = (int32_t)blockIdx.y;
-  const uint32_t columns = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+  const uint32_t columns = n <= 64 ? 64 : n <= 128 ? 128 : 256;
 
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(ready + 8 * i, 8);
       mbar_init(empty + 8 * i, 1);
+      mbar_init(ready + 8 * i, 8);
     }
     mbar_init(done, 1);
     failed_s = 0;
@@ -1050,15 +1075,10 @@ __global__ void __launch_bounds__(kOuterThreads)
   __syncthreads();
   fence_after();
   const uint32_t tmem = tmem_base;
+  const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, n) | kTransposeA | kTransposeB;
 
-  float unit = 1.0f;  // a power of two
-  if (!Widen<T>::kBf16) {
-    const uint32_t e = a.peak[id] >> 23;  // the largest is in [2^(e-127), 2^(e-126)): to [2^13, 2^14)
-    unit = __uint_as_float((e > 14 ? 267 - e : 253) << 23);
-  }
-  const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, n) | kTransposeA;
-
-  uint32_t seen = 0, used = 0;  // blocks of the adapter so far; those of this CTA
+  uint32_t seen = 0, used = 0;          // blocks of the adapter so far; those of this CTA
+  uint32_t s = 0, turn = 0;     // stage and parity of the next block
   bool ok = true;
   for (uint32_t w0 = 0; w0 < a.count; w0 += kWindow) {
     // this window's requests of the adapter, in order
@@ -1082,85 +1102,64 @@ __global__ void __launch_bounds__(kOuterThreads)
       end_s[at] = e;
     }
     __syncthreads();
-    for (uint32_t k = 0; k < total; ++k) {
+    for (uint32_t k = 0; k < total && ok; ++k) {
       const uint32_t blocks = (uint32_t)(end_s[k] - begin_s[k] + 63) / 64;
       // blocks seen, seen+1, ...: those with number % split == crank are this CTA's
-      for (uint32_t j = (crank + a.split - seen % a.split) % a.split; j < blocks; j += a.split, ++used) {
-        if (!ok) continue;
+      for (uint32_t j = (crank + a.split - seen % a.split) % a.split; j < blocks; j += a.split) {
         const int64_t t0 = (int64_t)begin_s[k] + 64 * (int64_t)j;
         const uint32_t valid = (uint32_t)min((int64_t)64, (int64_t)end_s[k] - t0);
-        const uint32_t s = used % a.stages, turn = used / a.stages, at = base + s * stage_bytes;
+        const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
         if (warp == 0) {
-          if (lane == 0) {
-            if (turn) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1, failed);
-            if (ok) {
-              mbar_expect(full + 8 * s, q_bytes);
-              tma_load(at, &map_q, (int32_t)c0, (int32_t)t0, full + 8 * s);
-              tma_load(at + 8192, &map_q, (int32_t)c0 + 64, (int32_t)t0, full + 8 * s);
-            }
+          ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+          if (!ok) break;
+          if (elect_one()) {
+            mbar_expect(bar, stage_bytes);
+            tma_load(at, map_q, (int32_t)c0, (int32_t)t0, bar);
+            tma_load(at + 8192, map_q, (int32_t)c0 + 64, (int32_t)t0, bar);
+            for (uint32_t x = 0; x < n; x += 64) tma_load(at + q_bytes + x * 128, map_p, (int32_t)x, (int32_t)t0, bar);
           }
+          __syncwarp();
         } else if (warp == 1) {
-          if (lane == 0) {
-            ok = mbar_wait(full + 8 * s, turn & 1, failed) && mbar_wait(ready + 8 * s, turn & 1, failed);
-            if (ok) {
-              fence_after();
-              const uint64_t q = desc_mn128(at, 8192), p = desc_k128(at + q_bytes);
+          ok = mbar_wait(ready + 8 * s, turn, failed);
+          if (!ok) break;
+          fence_after();
+          const uint64_t q = desc_mn128(at, 8192), p = desc_mn128(at + q_bytes, 8192);
+          if (elect_one()) {
 #pragma unroll
-              for (int m = 0; m < 4; ++m) mma_ss(tmem, q + m * 128, p + m * 2, idesc, used > 0 || m > 0);
-              mma_commit<1>(empty + 8 * s, 0);
-            }
+            for (int m = 0; m < 4; ++m) mma_ss(tmem, q + m * 128, p + m * 128, idesc, used > 0 || m > 0);
+            mma_commit<1>(empty + 8 * s, 0);
           }
+          __syncwarp();
         } else {
-          if (turn) ok = mbar_wait_warp(empty + 8 * s, (turn - 1) & 1, failed);
-          if (ok) {
-            for (uint32_t x = threadIdx.x - 64; x < a.rank * 8; x += 256) {
-              const uint32_t r = x % a.rank, t8 = x / a.rank;
-              const float* p = a.p + (uint64_t)(t0 + t8 * 8) * a.rank + r;
-              float v[8];
-#pragma unroll
-              for (uint32_t t = 0; t < 8; ++t) v[t] = t8 * 8 + t < valid ? p[t * a.rank] * unit : 0.0f;
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) split_pair<T>(v[2 * t], v[2 * t + 1], hi[t], lo[t]);
-              const uint32_t to = at + q_bytes + r * 128 + ((t8 ^ (r & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]),
-                           "r"(hi[3])
-                           : "memory");
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + pad * 128), "r"(lo[0]), "r"(lo[1]),
-                           "r"(lo[2]), "r"(lo[3])
-                           : "memory");
-            }
-            if (valid < 64) {
-              ok = mbar_wait_warp(full + 8 * s, turn & 1, failed);
-              // whole 128-byte rows, so the swizzle does not matter
-              for (uint32_t x = threadIdx.x - 64; x < (64 - valid) * 16; x += 256) {
-                const uint32_t to = at + (x / 8 % 2) * 8192 + (valid + x / 16) * 128 + x % 8 * 16;
-                if (ok) asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
-              }
+          ok = mbar_wait_warp(bar, turn, failed);
+          if (!ok) break;
+          if (valid < 64) {
+            // whole 128-byte rows, so the swizzle does not matter; boxes of 64 rows follow each other
+            const uint32_t boxes = 2 + n / 64;
+            for (uint32_t x = threadIdx.x - 64; x < (64 - valid) * boxes * 8; x += 256) {
+              const uint32_t box = x / 8 % boxes, r = valid + x / 8 / boxes, to = at + box * 8192 + r * 128 + x % 8 * 16;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to), "r"(0) : "memory");
             }
             fence_async();
-            __syncwarp();
-            if (ok && lane == 0) mbar_arrive(ready + 8 * s);
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + 8 * s);
         }
+        ++used;
+        if (++s == a.stages) s = 0, turn ^= 1;
       }
       seen += blocks;
     }
     __syncwarp();
     __syncthreads();
   }
-  if (warp == 0 && lane == 0 && used) {
-    // a CTA does not end while its loads are in flight
-    if (*failed)
-      for (uint32_t i = used > a.stages ? used - a.stages : 0; i < used; ++i) {
-        const long long start = clock64();
-        while (!mbar_try(full + 8 * (i % a.stages), (i / a.stages) & 1) && clock64() - start < kWaitCycles) {
-        }
-      }
+  if (warp == 0 && !ok) drain(full, s, turn, a.stages);
+  if (warp == 1 && used) {
+    if (ok && elect_one()) mma_commit<1>(done, 0);
+    __syncwarp();
   }
-  if (warp == 1 && lane == 0 && used && ok) mma_commit<1>(done, 0);
-  T* out = static_cast<T*>(a.out) + (uint64_t)id * a.f_adapter;
-  const float alpha = a.alpha[id] / unit;
+  T* out = static_cast<T*>(side.out) + (uint64_t)id * a.rank * side.cols;
+  const float alpha = a.alpha[id] / (Widen<T>::kBf16 ? 1.0f : unit_of(side.peak[id]));
   if (warp >= 2) {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     const uint32_t row = quarter * 32 + lane;
@@ -1180,18 +1179,18 @@ __global__ void __launch_bounds__(kOuterThreads)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((r0 + j) * 128 + row) * 4), "f"(d[j] + e[j]) : "memory");
-        } else if (c < a.cols) {
-          if (a.out_vector) {
+        } else if (c < side.cols) {
+          if (side.out_vector) {
             uint4 v;
             v.x = Widen<T>::pack((d[0] + e[0]) * alpha, (d[1] + e[1]) * alpha);
             v.y = Widen<T>::pack((d[2] + e[2]) * alpha, (d[3] + e[3]) * alpha);
             v.z = Widen<T>::pack((d[4] + e[4]) * alpha, (d[5] + e[5]) * alpha);
             v.w = Widen<T>::pack((d[6] + e[6]) * alpha, (d[7] + e[7]) * alpha);
-            *reinterpret_cast<uint4*>(out + c * a.sc + r0) = v;
+            *reinterpret_cast<uint4*>(out + c * side.sc + r0) = v;
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (r0 + j < a.rank) put(out + (r0 + j) * a.sr + c * a.sc, (d[j] + e[j]) * alpha);
+              if (r0 + j < a.rank) put(out + (r0 + j) * side.sr + c * side.sc, (d[j] + e[j]) * alpha);
           }
         }
       }
@@ -1208,7 +1207,7 @@ __global__ void __launch_bounds__(kOuterThreads)
         const float y[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (c + q < a.cols) put(out + r * a.sr + (c + q) * a.sc, y[q] * alpha);
+          if (c + q < side.cols) put(out + r * side.sr + (c + q) * side.sc, y[q] * alpha);
       }
     }
     __syncwarp();
@@ -1221,20 +1220,55 @@ __global__ void __launch_bounds__(kOuterThreads)
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
+// v (blockIdx.y = 0) and u (1), either of which may be absent: what is read, and what is written of it.
+struct PartsArgs {
+  const float* p[2];
+  uint32_t* peak[2];
+  void* parts[2];
+  uint64_t rows;
+  uint32_t rank;
+  const int32_t* row_id;
+};
+
 // peak[a] = bits of the largest finite |p| of adapter a's rows; peak starts at zero.  The order of the maxima does not
 // matter.
-__global__ void peak_kernel(const float* p, uint64_t rows, uint32_t rank, const int32_t* row_id, uint32_t* peak) {
-  const uint64_t warps = (uint64_t)gridDim.x * blockDim.x / 32;
-  for (uint64_t t = (blockIdx.x * (uint64_t)blockDim.x + threadIdx.x) / 32; t < rows; t += warps) {
-    const int32_t id = row_id[t];
+__global__ void __launch_bounds__(256) peak_kernel(PartsArgs a) {
+  const float* p = a.p[blockIdx.y];
+  if (!p) return;
+  const uint64_t warps = (uint64_t)gridDim.x * 8;
+  for (uint64_t t = blockIdx.x * 8 + threadIdx.x / 32; t < a.rows; t += warps) {
+    const int32_t id = a.row_id[t];
     if (id < 0) continue;
     float m = 0;
-    for (uint32_t r = threadIdx.x % 32; r < rank; r += 32) {
-      const float v = fabsf(p[t * rank + r]);
+    for (uint32_t r = threadIdx.x % 32; r < a.rank; r += 32) {
+      const float v = fabsf(p[t * a.rank + r]);
       if (isfinite(v)) m = fmaxf(m, v);
     }
     for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-    if (threadIdx.x % 32 == 0 && m > 0) atomicMax(peak + id, __float_as_uint(m));
+    if (threadIdx.x % 32 == 0 && m > 0) atomicMax(a.peak[blockIdx.y] + id, __float_as_uint(m));
+  }
+}
+
+// parts[t] = p[t] as 16-bit values, their rests and zeros; FP16 takes p times its adapter's power of two.
+template <class T>
+__global__ void __launch_bounds__(256) parts_kernel(PartsArgs a) {
+  const float* p = a.p[blockIdx.y];
+  if (!p) return;
+  const uint32_t pad = padded(a.rank), pairs = part_columns(a.rank) / 2;
+  uint32_t* out = static_cast<uint32_t*>(a.parts[blockIdx.y]);
+  const uint64_t total = a.rows * pairs, step = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += step) {
+    const uint64_t t = i / pairs;
+    const uint32_t c = (uint32_t)(i % pairs) * 2, r = c < pad ? c : c - pad;
+    const int32_t id = a.row_id[t];
+    uint32_t hi = 0, lo = 0;
+    if (id >= 0 && c < 2 * pad) {
+      const float unit = Widen<T>::kBf16 ? 1.0f : unit_of(a.peak[blockIdx.y][id]);
+      const float x = r < a.rank ? p[t * a.rank + r] * unit : 0.0f;
+      const float y = r + 1 < a.rank ? p[t * a.rank + r + 1] * unit : 0.0f;
+      split_pair<T>(x, y, hi, lo);
+    }
+    out[i] = c < pad ? hi : lo;
   }
 }
 
@@ -1272,7 +1306,7 @@ constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Plan {
-  size_t row_id, p, turned, peak, total;
+  size_t row_id, p, turned, peak, parts, total;
 };
 
 Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
@@ -1281,7 +1315,8 @@ Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
   w.p = up256(rows * 4);
   w.turned = w.p + up256(rows * lin->rank * 4);
   w.peak = w.turned + up256((size_t)lin->n_adapters * lin->rank * lin->n_out * 2);
-  w.total = w.peak + up256((size_t)lin->n_adapters * 8);
+  w.parts = w.peak + up256((size_t)lin->n_adapters * 8);
+  w.total = w.parts + 2 * up256(rows * part_columns(lin->rank) * 2);
   return w;
 }
 
@@ -1502,39 +1537,69 @@ int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint
   return cudaLaunchKernelEx(&cfg, shrink_tc<T>, mf, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
-// out[a] = alpha[a] * sum over a's rows of p[t] q[t], element (r, c) of an adapter at r * sr + c * sc.
+// One of the two gradients: out[a] = alpha[a] * sum over a's rows of p[t] q[t].
+struct Outer {
+  const void* q;
+  uint64_t q_stride, cols;
+  const float* p;
+  void* out;
+  uint64_t sr, sc;
+};
+
 template <class T>
-int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, uint32_t rank, const ecf8_requests* req,
-                 uint64_t rows, const uint32_t* peak, const float* alpha, uint32_t n_adapters, T* out,
-                 uint64_t f_adapter, uint64_t sr, uint64_t sc, int32_t* d_status, cudaStream_t s) {
+int outer_tensor(const Outer* sides, int n_sides, uint32_t rank, uint32_t n_adapters, const ecf8_requests* req,
+                 uint64_t rows, const int32_t* row_id, uint32_t* peak, char* parts, const float* alpha,
+                 int32_t* d_status, cudaStream_t s) {
   static bool set[64] = {};
   if (const int rc = allow_smem(outer_tc<T>, set)) return rc;
+  const CUtensorMapDataType type =
+      Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint32_t columns = part_columns(rank);
+  const size_t part_bytes = up256(rows * columns * 2);
   OuterArgs a{};
   a.rows = rows;
-  a.cols = cols;
   a.rank = rank;
-  a.p = p;
   a.offsets = req->d_offsets;
   a.ids = req->d_ids;
   a.count = req->count;
-  a.peak = peak;
   a.alpha = alpha;
-  a.out = out;
-  a.f_adapter = f_adapter;
-  a.sr = sr;
-  a.sc = sc;
-  a.out_vector = sr == 1 && rank % 8 == 0 && aligned(out, 16);
   a.status = d_status;
-  const uint64_t tiles = (cols + 127) / 128;
+  PartsArgs b{};
+  b.rows = rows;
+  b.rank = rank;
+  b.row_id = row_id;
+  CUtensorMap maps[4];
+  uint64_t tiles = 0;
+  for (int i = 0; i < n_sides; ++i) {
+    const Outer& o = sides[i];
+    OuterSide& d = a.side[i];
+    d.cols = o.cols;
+    d.tiles = (uint32_t)((o.cols + 127) / 128);
+    d.peak = peak + i * n_adapters;
+    d.out = o.out;
+    d.sr = o.sr;
+    d.sc = o.sc;
+    d.out_vector = o.sr == 1 && rank % 8 == 0 && aligned(o.out, 16);
+    tiles += d.tiles;
+    b.p[i] = o.p;
+    b.peak[i] = peak + i * n_adapters;
+    b.parts[i] = parts + i * part_bytes;
+    if (!make_map(&maps[2 * i], type, o.q, o.cols, rows, o.q_stride * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&maps[2 * i + 1], type, b.parts[i], columns, rows, columns * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+      return ECF8_ERR_CUDA;
+  }
+  for (int i = n_sides; i < 2; ++i) maps[2 * i] = maps[0], maps[2 * i + 1] = maps[1];
+  if (!Widen<T>::kBf16) {
+    if (cudaMemsetAsync(peak, 0, (size_t)n_adapters * 8, s) != cudaSuccess) return ECF8_ERR_CUDA;
+    peak_kernel<<<dim3((unsigned)((rows + 7) / 8 < 592 ? (rows + 7) / 8 : 592), n_sides), 256, 0, s>>>(b);
+  }
+  const uint64_t blocks = (rows * columns / 2 + 255) / 256;
+  parts_kernel<T><<<dim3((unsigned)(blocks < 1184 ? blocks : 1184), n_sides), 256, 0, s>>>(b);
   a.split = 1;
-  while (a.split < 8 && tiles * n_adapters * a.split * 2 <= 148 && rows / (64 * a.split * 2) >= 2) a.split *= 2;
-  const uint32_t pad = (rank + 7) / 8 * 8, stage = 16384 + pad * 256;
-  a.stages = (218 * 1024 - 1024) / stage < 8 ? (218 * 1024 - 1024) / stage : 8;
-  const size_t smem = (size_t)a.stages * stage + 1024;  // at least the sums, pad * 512 bytes
-  CUtensorMap mq;
-  if (!make_map(&mq, Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, cols,
-                rows, q_stride * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
-    return ECF8_ERR_CUDA;
+  while (a.split < 8 && tiles * n_adapters * a.split * 2 <= 296 && rows / (64 * a.split * 2) >= 2) a.split *= 2;
+  const uint32_t stage = 16384 + columns * 128;
+  a.stages = 106 * 1024 / stage < kMaxStages ? 106 * 1024 / stage : kMaxStages;
+  const size_t smem = (size_t)a.stages * stage + 1024;  // at least the sums, 512 bytes a rank
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * a.split), n_adapters);
   cfg.blockDim = dim3(kOuterThreads);
@@ -1546,7 +1611,8 @@ int outer_tensor(const T* q, uint64_t q_stride, uint64_t cols, const float* p, u
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, outer_tc<T>, mq, a) == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, outer_tc<T>, maps[0], maps[1], maps[2], maps[3], a) == cudaSuccess ? ECF8_OK
+                                                                                                     : ECF8_ERR_CUDA;
 }
 
 template <class T, int BACK>
@@ -1630,33 +1696,23 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   const uint32_t count = adapted ? q->count : 0;
   const int32_t* offsets = adapted ? q->d_offsets : nullptr;
   const int32_t* ids = adapted ? q->d_ids : nullptr;
-  const bool fp16 = l->dtype == ECF8_DTYPE_FP16;
-  uint32_t* peak = reinterpret_cast<uint32_t*>(ws + w.peak);  // of v, then of u
-  const bool da_tensor = da && adapted && tensor_path(l, x, x_stride), db_tensor = db && adapted && tensor_path(l, dy, dy_stride);
-  if (fp16 && (da_tensor || db_tensor)) {
-    if (cudaMemsetAsync(peak, 0, (size_t)l->n_adapters * 8, s) != cudaSuccess) return ECF8_ERR_CUDA;
-    const unsigned grid = (unsigned)((rows + 7) / 8 < 592 ? (rows + 7) / 8 : 592);
-    if (da_tensor) peak_kernel<<<grid, 256, 0, s>>>(v, rows, l->rank, row_id, peak);
-    if (db_tensor) peak_kernel<<<grid, 256, 0, s>>>(u, rows, l->rank, row_id, peak + l->n_adapters);
+  const Outer sides[2] = {{x, x_stride, l->k_in, v, da, l->k_in, 1}, {dy, dy_stride, l->n_out, u, db, 1, l->rank}};
+  Outer fast[2];
+  int n_fast = 0;
+  for (const Outer& o : sides) {
+    if (!o.out) continue;
+    if (adapted && tensor_path(l, o.q, o.q_stride)) {
+      fast[n_fast++] = o;
+      continue;
+    }
+    outer_simple<T><<<dim3((unsigned)((o.cols + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
+        o.p, l->rank, static_cast<const T*>(o.q), o.q_stride, o.cols, offsets, ids, count, rows, l->d_alpha,
+        static_cast<T*>(o.out), l->rank * o.cols, o.sr, o.sc);
   }
-  if (da_tensor) {
-    const int rc = outer_tensor<T>(static_cast<const T*>(x), x_stride, l->k_in, v, l->rank, q, rows, peak, l->d_alpha,
-                                   l->n_adapters, static_cast<T*>(da), l->rank * l->k_in, l->k_in, 1, d_status, s);
+  if (n_fast) {
+    const int rc = outer_tensor<T>(fast, n_fast, l->rank, l->n_adapters, q, rows, row_id,
+                                   reinterpret_cast<uint32_t*>(ws + w.peak), ws + w.parts, l->d_alpha, d_status, s);
     if (rc) return rc;
-  } else if (da) {
-    outer_simple<T><<<dim3((unsigned)((l->k_in + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
-        v, l->rank, static_cast<const T*>(x), x_stride, l->k_in, offsets, ids, count, rows, l->d_alpha,
-        static_cast<T*>(da), l->rank * l->k_in, l->k_in, 1);
-  }
-  if (db_tensor) {
-    const int rc = outer_tensor<T>(static_cast<const T*>(dy), dy_stride, l->n_out, u, l->rank, q, rows,
-                                   peak + l->n_adapters, l->d_alpha, l->n_adapters, static_cast<T*>(db),
-                                   l->rank * l->n_out, 1, l->rank, d_status, s);
-    if (rc) return rc;
-  } else if (db) {
-    outer_simple<T><<<dim3((unsigned)((l->n_out + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
-        u, l->rank, static_cast<const T*>(dy), dy_stride, l->n_out, offsets, ids, count, rows, l->d_alpha,
-        static_cast<T*>(db), l->rank * l->n_out, 1, l->rank);
   }
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }

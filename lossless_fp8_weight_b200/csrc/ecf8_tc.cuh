@@ -178,7 +178,7 @@ __device__ inline uint64_t desc_mn128(uint32_t addr, uint32_t next) {
   return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
-constexpr uint32_t kTransposeA = 1u << 15;  // in the instruction descriptor: A is desc_mn128
+constexpr uint32_t kTransposeA = 1u << 15, kTransposeB = 1u << 16;  // in the instruction descriptor: A, B is desc_mn128
 
 // 16-bit inputs of one type, float32 sums, m x n; both operands with the reduction contiguous.
 __host__ __device__ inline uint32_t idesc_f16(bool bf16, uint32_t m, uint32_t n) {
