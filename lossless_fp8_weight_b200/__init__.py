@@ -304,7 +304,7 @@ def _nbytes(t, default: int) -> int:
 def _stream(stream) -> int:
     if stream is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return int(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

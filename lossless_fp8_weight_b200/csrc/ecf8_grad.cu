@@ -14,8 +14,14 @@
 // from there.  Squares are summed in float64 (a float32 squared is exact in it,
 // and no norm that is finite overflows), per thread, then per CTA in a fixed
 // tree, then over the CTAs' sums in index order, so the result does not vary.
-// The second launch sums the CTAs' partial sums in every CTA for itself, which
-// needs no barrier across the grid.
+// Conversions to float64 run at some 5 values a clock and SM, which for 16-bit
+// values is half of what memory delivers: four of those are squared exactly and
+// added in pairs in float32 first (two roundings, 2^-24 of the norm), unless
+// the sum is outside what float32 holds without loss.  The second launch sums
+// the CTAs' partial sums in every CTA for itself, which needs no barrier across
+// the grid, and starts beside the end of the first.
+//
+// Measured: 448 BF16 tensors, 42M values: norm 30 us with float64 alone.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,6 +53,8 @@ struct Entry {
 
 __host__ __device__ inline uint32_t width(int32_t dtype) { return dtype == ECF8_DTYPE_FP32 ? 4 : 2; }
 
+template <int N> struct Count { static constexpr int value = N; };
+
 template <int DT> struct Type;
 template <> struct Type<ECF8_DTYPE_BF16> {
   using T = __nv_bfloat16;
@@ -67,23 +75,20 @@ template <> struct Type<ECF8_DTYPE_FP32> {
   static __device__ T put(float v) { return v; }
 };
 
-// The index of the tensor that holds a chunk: the last entry whose first chunk
-// is not past it and that has chunks.
+// The index of the tensor that holds a chunk: the last entry whose first chunk is not past it.  The threads look at
+// every entry at once: a binary search would wait for memory ten times.
 __device__ uint32_t find(const Entry* e, uint32_t count, uint64_t chunk) {
-  uint32_t lo = 0, hi = count - 1;
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi + 1) / 2;
-    if (e[mid].first_chunk <= chunk) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+  uint32_t upto = 0;
+  for (uint32_t i = 0; i < count; i += kThreads)
+    upto += __syncthreads_count(i + threadIdx.x < count && e[i + threadIdx.x].first_chunk <= chunk);
+  return upto - 1;  // the first entry's is 0
 }
 
-// Calls f(entry, begin, end) for the CTA's run of chunks, tensor by tensor.
+// Calls f(entry, begin, end) for run `cta` of chunks, tensor by tensor.
 template <class F>
-__device__ void walk(const Entry* e, uint32_t count, uint64_t chunks, F f) {
-  uint64_t c = chunks * blockIdx.x / gridDim.x;
-  const uint64_t last = chunks * (blockIdx.x + 1) / gridDim.x;
+__device__ void walk(const Entry* e, uint32_t count, uint64_t chunks, uint32_t cta, F f) {
+  uint64_t c = chunks * cta / gridDim.x;
+  const uint64_t last = chunks * (cta + 1) / gridDim.x;
   if (c >= last) return;
   for (uint32_t i = find(e, count, c); i < count && c < last; ++i) {
     const Entry t = e[i];
@@ -114,6 +119,30 @@ __device__ double squares(const Entry& t, uint64_t b, uint64_t end) {
     const double d = (double)Type<DT>::get(v);
     s = fma(d, d, s);
   };
+  auto vector = [&](const uint4& w) {
+    const T* v = reinterpret_cast<const T*>(&w);
+    if (V == 4) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) one(v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        const float x0 = Type<DT>::get(v[j]), x1 = Type<DT>::get(v[j + 1]), x2 = Type<DT>::get(v[j + 2]),
+                    x3 = Type<DT>::get(v[j + 3]);
+        const float q = fmaf(x1, x1, x0 * x0) + fmaf(x3, x3, x2 * x2);
+        if (q >= 0x1p-90f && q <= 0x1p120f) {
+          // a normal float32 as float64, by its bits: the conversion has a quarter of the rate
+          const uint32_t bits = __float_as_uint(q);
+          s += __hiloint2double((int)((bits >> 3) + 0x38000000u), (int)(bits << 29));
+        } else {
+          one(v[j]);
+          one(v[j + 1]);
+          one(v[j + 2]);
+          one(v[j + 3]);
+        }
+      }
+    }
+  };
   if (threadIdx.x < head) one(p[threadIdx.x]);
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
   const uint64_t nv = (n - head) / V;
@@ -123,18 +152,9 @@ __device__ double squares(const Entry& t, uint64_t b, uint64_t end) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = q[i + k * kThreads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const T* v = reinterpret_cast<const T*>(&w[k]);
-#pragma unroll
-      for (int j = 0; j < V; ++j) one(v[j]);
-    }
+    for (int k = 0; k < 4; ++k) vector(w[k]);
   }
-  for (; i < nv; i += kThreads) {
-    const uint4 w = q[i];
-    const T* v = reinterpret_cast<const T*>(&w);
-#pragma unroll
-    for (int j = 0; j < V; ++j) one(v[j]);
-  }
+  for (; i < nv; i += kThreads) vector(q[i]);
   const uint64_t tail = head + nv * V;
   if (tail + threadIdx.x < n) one(p[tail + threadIdx.x]);
   return s;
@@ -165,28 +185,24 @@ __device__ void scaled(const Entry& t, uint64_t b, uint64_t end, float factor) {
   const uint4* q = reinterpret_cast<const uint4*>(p + head);
   uint4* r = reinterpret_cast<uint4*>(o + head);
   const uint64_t nv = (n - head) / V;
-  uint64_t i = threadIdx.x;
-  for (; i + 3 * kThreads < nv; i += 4 * kThreads) {
-    uint4 w[4];
+  // read and written for the last time here: other data should stay in L2
+  auto vectors = [&](uint64_t i, auto n_vectors) {
+    constexpr int N = decltype(n_vectors)::value;
+    uint4 w[N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = q[i + k * kThreads];
+    for (int k = 0; k < N; ++k) w[k] = __ldcs(q + i + k * kThreads);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < N; ++k) {
       T* v = reinterpret_cast<T*>(&w[k]);
       if (!copy)
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = one(v[j]);
-      r[i + k * kThreads] = w[k];
+      __stcs(r + i + k * kThreads, w[k]);
     }
-  }
-  for (; i < nv; i += kThreads) {
-    uint4 w = q[i];
-    T* v = reinterpret_cast<T*>(&w);
-    if (!copy)
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = one(v[j]);
-    r[i] = w;
-  }
+  };
+  uint64_t i = threadIdx.x;
+  for (; i + 3 * kThreads < nv; i += 4 * kThreads) vectors(i, Count<4>{});
+  for (; i < nv; i += kThreads) vectors(i, Count<1>{});
   const uint64_t tail = head + nv * V;
   if (tail + threadIdx.x < n) single(tail + threadIdx.x);
 }
@@ -205,9 +221,10 @@ __device__ double block_sum(double s) {
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const Header* table, uint32_t count, uint64_t chunks,
                                                         double* partial) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Entry* e = reinterpret_cast<const Entry*>(table + 1);
   double s = 0;
-  walk(e, count, chunks, [&](const Entry& t, uint64_t b, uint64_t end) {
+  walk(e, count, chunks, blockIdx.x, [&](const Entry& t, uint64_t b, uint64_t end) {
     if (t.dtype == ECF8_DTYPE_BF16) s += squares<ECF8_DTYPE_BF16>(t, b, end);
     else if (t.dtype == ECF8_DTYPE_FP16) s += squares<ECF8_DTYPE_FP16>(t, b, end);
     else s += squares<ECF8_DTYPE_FP32>(t, b, end);
@@ -219,6 +236,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const Header* table, uin
 __global__ void __launch_bounds__(kThreads) clip_kernel(const Header* table, uint32_t count, uint64_t chunks,
                                                         const double* partial, uint32_t n_partial, float max_norm,
                                                         int clip, float* d_norm, int32_t* d_status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   double s = 0;
   for (uint32_t i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
   const double norm = sqrt(block_sum(s));
@@ -231,7 +249,8 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const Header* table, uin
   if (!clip) return;
   const float factor = finite ? (float)fmin(1.0, (double)max_norm / (norm + 1e-6)) : 1.0f;
   const Entry* e = reinterpret_cast<const Entry*>(table + 1);
-  walk(e, count, chunks, [&](const Entry& t, uint64_t b, uint64_t end) {
+  // what the norm read last is in L2 still: the runs are taken from the end
+  walk(e, count, chunks, gridDim.x - 1 - blockIdx.x, [&](const Entry& t, uint64_t b, uint64_t end) {
     if (factor == 1.0f && t.in == t.out) return;  // x * 1 is there already
     if (t.dtype == ECF8_DTYPE_BF16) scaled<ECF8_DTYPE_BF16>(t, b, end, factor);
     else if (t.dtype == ECF8_DTYPE_FP16) scaled<ECF8_DTYPE_FP16>(t, b, end, factor);
@@ -259,8 +278,18 @@ int run(const void* h_table, const void* d_table, int clip, float max_norm, floa
   const Header* d = static_cast<const Header*>(d_table);
   double* partial = static_cast<double*>(ws);
   if (grid) norm_kernel<<<(unsigned)grid, kThreads, 0, s>>>(d, h->count, h->chunks, partial);
-  clip_kernel<<<clip && grid ? (unsigned)grid : 1, kThreads, 0, s>>>(d, h->count, h->chunks, partial, (uint32_t)grid,
-                                                                      max_norm, clip && grid, d_norm, d_status);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(clip && grid ? (unsigned)grid : 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = grid ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, clip_kernel, d, (uint32_t)h->count, (uint64_t)h->chunks, (const double*)partial,
+                         (uint32_t)grid, max_norm, (int)(clip && grid), d_norm, d_status) != cudaSuccess)
+    return ECF8_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
 
