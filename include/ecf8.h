@@ -347,9 +347,11 @@ void ecf8_pipeline_destroy(ecf8_pipeline* p);
  * x, y, A, B and the gradients are all of one type, BF16 or FP16 (d_w is
  * always E4M3, scales and alpha float32).  Products are summed in float32 and
  * rounded once, when a result is written.  Rows of x, y and W may be strided;
- * every pointer needs the alignment of its type, and sizes may be odd.
- * (BF16/FP16 pointers and row strides of 16 bytes, and d_w and w_stride of 16,
- * take the tensor-core path when k_in and n_out are multiples of 16.)
+ * every pointer needs the alignment of its type, and sizes may be odd.  The
+ * tensor-core kernels read W, x, dy and A where their rows start at multiples
+ * of 16 bytes; an operand whose rows do not is copied into the workspace first
+ * (x and dy where k_in or n_out is no multiple of 8; where only their strides
+ * or pointers are in the way, slower kernels take them as they are).
  * Outputs must not overlap inputs.  E4M3 NaN bytes count as NaN.  A row's
  * result depends on its own row of x and its own adapter only: an adapter that
  * holds infinities or NaN leaves the other requests' rows as they would be.
@@ -385,7 +387,9 @@ typedef struct ecf8_requests {
 } ecf8_requests;
 
 /* Bytes of device workspace a forward or backward call of this many rows
- * needs (0 without adapters). */
+ * needs.  Without adapters it is for copies of operands alone: 0 where their
+ * rows start at multiples of 16 bytes, and a call that is given none takes
+ * the slower kernels. */
 size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows);
 
 /* y = s * (x W^T) + the adapters' part, for `rows` rows.  requests may be NULL

@@ -966,6 +966,36 @@ __global__ void __launch_bounds__(kShrinkThreads)
   if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
+// Rows of bytes copied to rows whose bases and distances TMA takes (multiples of 16 bytes), for operands that are
+// not laid out so.  A thread writes 16 bytes: the source is read in aligned 4-byte words and shifted into place.
+struct Restride {
+  const uint8_t* from[3];
+  uint8_t* to[3];
+  uint64_t rows[3], bytes[3], stride[3], to_stride[3];  // in bytes
+};
+
+__global__ void __launch_bounds__(256) restride_kernel(Restride a) {
+  const int k = blockIdx.y;
+  const uint64_t per = a.to_stride[k] / 16, total = a.rows[k] * per, step = (uint64_t)gridDim.x * 256;
+  for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += step) {
+    const uint64_t row = i / per, at = i % per * 16;
+    const uint8_t* src = a.from[k] + row * a.stride[k] + at;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>((uintptr_t)src & ~(uintptr_t)3);
+    const uint32_t shift = ((uintptr_t)src & 3) * 8;
+    // bytes of this piece that exist, and the words that hold one of them
+    const int64_t left = min((int64_t)16, (int64_t)a.bytes[k] - (int64_t)at), held = (left + shift / 8 + 3) / 4;
+    uint32_t w[5], v[4];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = j < held ? words[j] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = __funnelshift_r(w[j], w[j + 1], shift);
+      if (left < 4 * j + 4) v[j] = left <= 4 * j ? 0 : v[j] & (0xffffffffu >> (32 - 8 * (left - 4 * j)));
+    }
+    *reinterpret_cast<uint4*>(a.to[k] + row * a.to_stride[k] + at) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+}
+
 // out[a][r][j] = in[a][j][r]: B with the reduction of dy B contiguous, as the kernel above reads it.
 template <class T>
 __global__ void __launch_bounds__(256) transpose_kernel(const T* in, T* out, uint64_t len, uint64_t out_len,
@@ -1305,21 +1335,48 @@ constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+bool aligned(const void* p, uint64_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// Whether TMA can read rows of `width`-byte values from here.
+bool tma_rows(const void* p, uint64_t stride, uint64_t width) { return aligned(p, 16) && stride * width % 16 == 0; }
+
+// The workspace: sections of a call of this many rows.  Operands whose rows TMA cannot read have a place for a copy
+// (x and dy by their length alone: that of rows without gaps).
 struct Plan {
-  size_t row_id, p, turned, peak, parts, total;
+  size_t row_id, p, turned, peak, parts, copies, total;
+  uint64_t w_stride, x_stride, dy_stride, a_stride, b_stride;  // rows of the copies, in values
+  size_t w, x, dy, a;
 };
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 Plan plan_of(const ecf8_linear* lin, uint64_t rows) {
   Plan w{};
-  if (!lin->n_adapters) return w;
-  w.p = up256(rows * 4);
-  w.turned = w.p + up256(rows * lin->rank * 4);
-  w.peak = w.turned + up256((size_t)lin->n_adapters * lin->rank * lin->n_out * 2);
-  w.parts = w.peak + up256((size_t)lin->n_adapters * 8);
-  w.total = w.parts + 2 * up256(rows * part_columns(lin->rank) * 2);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += up256(bytes);
+    return from;
+  };
+  w.w_stride = up(lin->k_in, 16);
+  w.x_stride = w.a_stride = up(lin->k_in, 8);
+  w.dy_stride = w.b_stride = up(lin->n_out, 8);
+  const uint64_t factors = (uint64_t)lin->n_adapters * lin->rank;
+  if (lin->n_adapters) {
+    w.row_id = take(rows * 4);
+    w.p = take(rows * lin->rank * 4);
+    w.turned = take(factors * w.b_stride * 2);
+    w.peak = take((size_t)lin->n_adapters * 8);
+    w.parts = take(2 * up256(rows * part_columns(lin->rank) * 2));
+  }
+  w.copies = at;
+  w.w = take(tma_rows(lin->d_w, lin->w_stride, 1) ? 0 : lin->n_out * w.w_stride);
+  w.x = take(lin->k_in % 8 ? rows * w.x_stride * 2 : 0);
+  w.dy = take(lin->n_out % 8 ? rows * w.dy_stride * 2 : 0);
+  if (lin->n_adapters) w.a = take(tma_rows(lin->d_a, lin->k_in, 2) ? 0 : factors * w.a_stride * 2);
+  w.total = at;
   return w;
 }
-
 
 int check(const ecf8_linear* l, const ecf8_requests* q, uint64_t rows, const void* ws, size_t ws_bytes,
           const int32_t* d_status) {
@@ -1330,16 +1387,18 @@ int check(const ecf8_linear* l, const ecf8_requests* q, uint64_t rows, const voi
   if (l->n_scale != 0 && l->n_scale != 1 && l->n_scale != l->n_out) return ECF8_ERR_ARG;
   if (!l->d_w || (l->n_scale && !l->d_scale)) return ECF8_ERR_ARG;
   if (((uintptr_t)l->d_scale | (uintptr_t)d_status) & 3) return ECF8_ERR_ALIGN;
-  if (!l->n_adapters) return ECF8_OK;
-  if (l->n_adapters >= 65536 || l->rank < 1 || l->rank > ECF8_RANK_MAX) return ECF8_ERR_ARG;
-  if (!l->d_a || !l->d_b || !l->d_alpha) return ECF8_ERR_ARG;
-  if ((((uintptr_t)l->d_a | (uintptr_t)l->d_b) & 1) || ((uintptr_t)l->d_alpha & 3)) return ECF8_ERR_ALIGN;
-  if (q && q->count) {
-    if (q->count >= kMost || !q->d_offsets || !q->d_ids) return ECF8_ERR_ARG;
-    if (((uintptr_t)q->d_offsets | (uintptr_t)q->d_ids) & 3) return ECF8_ERR_ALIGN;
+  if (l->n_adapters) {
+    if (l->n_adapters >= 65536 || l->rank < 1 || l->rank > ECF8_RANK_MAX) return ECF8_ERR_ARG;
+    if (!l->d_a || !l->d_b || !l->d_alpha) return ECF8_ERR_ARG;
+    if ((((uintptr_t)l->d_a | (uintptr_t)l->d_b) & 1) || ((uintptr_t)l->d_alpha & 3)) return ECF8_ERR_ALIGN;
+    if (q && q->count) {
+      if (q->count >= kMost || !q->d_offsets || !q->d_ids) return ECF8_ERR_ARG;
+      if (((uintptr_t)q->d_offsets | (uintptr_t)q->d_ids) & 3) return ECF8_ERR_ALIGN;
+    }
   }
+  // without adapters a workspace is for copies alone, and none means no copies
   const size_t need = plan_of(l, rows).total;
-  if (need && (!ws || ws_bytes < need)) return ECF8_ERR_WORKSPACE;
+  if (ws ? ws_bytes < need : l->n_adapters && need) return ECF8_ERR_WORKSPACE;
   if ((uintptr_t)ws & 15) return ECF8_ERR_ALIGN;
   return ECF8_OK;
 }
@@ -1378,14 +1437,66 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* at, uint64
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned(const void* p, uint64_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// Where a call's operands are read from: themselves, or copies whose rows TMA can read.
+struct Operands {
+  ecf8_linear l;         // the weight in place of the caller's
+  const void* a;         // A, rows a_stride apart
+  uint64_t a_stride;
+  const void *x, *dy;
+  uint64_t x_stride, dy_stride;
+  bool weight, factor;   // TMA can read the weight, A
+};
 
-// TMA moves 16-byte units: bases, row strides and row lengths have to be multiples of it.  Row lengths: the map's inner
-// extent may be any, but the next row's first bytes must not be reached by a box that starts inside, which a
-// multiple of 16 values keeps out for both types.
-bool tensor_path(const ecf8_linear* l, const void* q, uint64_t q_stride) {
-  return l->k_in % 16 == 0 && l->n_out % 16 == 0 && l->k_in < (1u << 24) && l->n_out < (1u << 24) &&
-         aligned(l->d_w, 16) && l->w_stride % 16 == 0 && aligned(q, 16) && q_stride % 8 == 0;
+bool small_enough(const ecf8_linear& l) { return l.k_in < (1u << 24) && l.n_out < (1u << 24); }
+
+// Copies what has to be copied and can be.
+template <class T>
+int lay_out(const ecf8_linear* l, const Plan& w, char* ws, const void* x, uint64_t x_stride, const void* dy,
+            uint64_t dy_stride, uint64_t rows, bool use_a, Operands* o, cudaStream_t s) {
+  *o = Operands{*l, l->d_a, l->k_in, x, dy, x_stride, dy_stride, tma_rows(l->d_w, l->w_stride, 1),
+                use_a && tma_rows(l->d_a, l->k_in, 2)};
+  if (!ws || !small_enough(*l)) return ECF8_OK;
+  Restride r{};
+  int n = 0;
+  auto copy = [&](const void* from, uint64_t n_rows, uint64_t len, uint64_t stride, size_t to, uint64_t to_stride,
+                  uint64_t width) -> void* {
+    r.from[n] = static_cast<const uint8_t*>(from);
+    r.to[n] = reinterpret_cast<uint8_t*>(ws + to);
+    r.rows[n] = n_rows;
+    r.bytes[n] = len * width;
+    r.stride[n] = stride * width;
+    r.to_stride[n] = to_stride * width;
+    return r.to[n++];
+  };
+  if (!o->weight) {
+    o->l.d_w = static_cast<const uint8_t*>(copy(l->d_w, l->n_out, l->k_in, l->w_stride, w.w, w.w_stride, 1));
+    o->l.w_stride = w.w_stride;
+    o->weight = true;
+  }
+  if (x && l->k_in % 8 && !tma_rows(x, x_stride, 2)) {
+    o->x = copy(x, rows, l->k_in, x_stride, w.x, w.x_stride, 2);
+    o->x_stride = w.x_stride;
+  }
+  if (dy && l->n_out % 8 && !tma_rows(dy, dy_stride, 2)) {
+    o->dy = copy(dy, rows, l->n_out, dy_stride, w.dy, w.dy_stride, 2);
+    o->dy_stride = w.dy_stride;
+  }
+  if (use_a && !o->factor && n < 3) {
+    o->a = copy(l->d_a, (uint64_t)l->n_adapters * l->rank, l->k_in, l->k_in, w.a, w.a_stride, 2);
+    o->a_stride = w.a_stride;
+    o->factor = true;
+  }
+  if (n) {
+    uint64_t most = 0;
+    for (int i = 0; i < n; ++i) most = most > r.rows[i] * r.to_stride[i] ? most : r.rows[i] * r.to_stride[i];
+    const uint64_t blocks = (most / 16 + 255) / 256;
+    restride_kernel<<<dim3((unsigned)(blocks < 1184 ? blocks : 1184), n), 256, 0, s>>>(r);
+  }
+  return ECF8_OK;
+}
+
+bool tensor_path(const Operands& o, const void* q, uint64_t q_stride) {
+  return o.weight && small_enough(o.l) && tma_rows(q, q_stride, 2);
 }
 
 template <class K>
@@ -1461,7 +1572,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.p_vector = l->rank % 4 == 0 && aligned(p, 16);
   a.out = out;
   a.out_stride = out_stride;
-  a.out_vector = aligned(out, 8) && out_stride % 4 == 0;
+  a.out_vector = aligned(out, 8) && out_stride % 4 == 0 && cols % 4 == 0;
   a.status = d_status;
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -1616,9 +1727,10 @@ int outer_tensor(const Outer* sides, int n_sides, uint32_t rank, uint32_t n_adap
 }
 
 template <class T, int BACK>
-int product(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
+int product(const Operands& o, bool adapted, const void* in, uint64_t in_stride, void* out, uint64_t out_stride,
             uint64_t rows, const int32_t* row_id, const float* p, bool overlap, int32_t* d_status, cudaStream_t s) {
-  if (tensor_path(l, in, in_stride))
+  const ecf8_linear* l = &o.l;
+  if (tensor_path(o, in, in_stride))
     return product_tensor<T, BACK>(l, adapted, in, in_stride, out, out_stride, rows, row_id, p, overlap, d_status, s);
   const uint64_t cols = BACK ? l->k_in : l->n_out, len = BACK ? l->n_out : l->k_in;
   const uint64_t step = kGridY * 64;
@@ -1642,9 +1754,11 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   const bool keep = u != nullptr;
   bool overlap = false;  // the projection may start beside the kernel before it
   if (l->n_adapters && !u) u = reinterpret_cast<float*>(ws + w.p);
+  Operands o;
+  if (const int rc = lay_out<T>(l, w, ws, x, x_stride, nullptr, 0, rows, adapted, &o, s)) return rc;
   if (adapted) {
-    if (tensor_path(l, x, x_stride) && aligned(l->d_a, 16)) {
-      const int rc = shrink_tensor<T>(static_cast<const T*>(x), x_stride, rows, static_cast<const T*>(l->d_a), l->k_in,
+    if (tensor_path(o, o.x, o.x_stride) && o.factor) {
+      const int rc = shrink_tensor<T>(static_cast<const T*>(o.x), o.x_stride, rows, static_cast<const T*>(o.a), o.a_stride,
                                       l->k_in, l->n_adapters, l->rank, q, row_id, u, d_status, s);
       if (rc) return rc;
       overlap = true;
@@ -1657,7 +1771,7 @@ int forward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64_
   } else if (l->n_adapters && keep) {
     if (cudaMemsetAsync(u, 0, rows * l->rank * 4, s) != cudaSuccess) return ECF8_ERR_CUDA;
   }
-  const int rc = product<T, 0>(l, adapted, x, x_stride, y, y_stride, rows, row_id, u, overlap, d_status, s);
+  const int rc = product<T, 0>(o, adapted, o.x, o.x_stride, y, y_stride, rows, row_id, u, overlap, d_status, s);
   if (rc) return rc;
   return cudaGetLastError() == cudaSuccess ? ECF8_OK : ECF8_ERR_CUDA;
 }
@@ -1671,12 +1785,15 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
   int32_t* row_id = reinterpret_cast<int32_t*>(ws);
   float* v = reinterpret_cast<float*>(ws + w.p);
   bool overlap = false;
+  Operands o;
+  if (rows)
+    if (const int rc = lay_out<T>(l, w, ws, da ? x : nullptr, x_stride, dy, dy_stride, rows, false, &o, s)) return rc;
   if (adapted && (dx || da)) {
-    if (tensor_path(l, dy, dy_stride)) {
+    if (tensor_path(o, o.dy, o.dy_stride)) {
       T* turned = reinterpret_cast<T*>(ws + w.turned);
       transpose_kernel<T><<<dim3((unsigned)((l->n_out + 63) / 64), l->n_adapters), 256, 0, s>>>(
-          static_cast<const T*>(l->d_b), turned, l->n_out, l->n_out, l->rank);
-      const int rc = shrink_tensor<T>(static_cast<const T*>(dy), dy_stride, rows, turned, l->n_out, l->n_out,
+          static_cast<const T*>(l->d_b), turned, l->n_out, w.b_stride, l->rank);
+      const int rc = shrink_tensor<T>(static_cast<const T*>(o.dy), o.dy_stride, rows, turned, w.b_stride, l->n_out,
                                       l->n_adapters, l->rank, q, row_id, v, d_status, s);
       if (rc) return rc;
       overlap = true;
@@ -1690,24 +1807,25 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
     route(l, q, rows, row_id, d_status, s);
   }
   if (dx && rows) {
-    const int rc = product<T, 1>(l, adapted, dy, dy_stride, dx, dx_stride, rows, row_id, v, overlap, d_status, s);
+    const int rc = product<T, 1>(o, adapted, o.dy, o.dy_stride, dx, dx_stride, rows, row_id, v, overlap, d_status, s);
     if (rc) return rc;
   }
   const uint32_t count = adapted ? q->count : 0;
   const int32_t* offsets = adapted ? q->d_offsets : nullptr;
   const int32_t* ids = adapted ? q->d_ids : nullptr;
-  const Outer sides[2] = {{x, x_stride, l->k_in, v, da, l->k_in, 1}, {dy, dy_stride, l->n_out, u, db, 1, l->rank}};
+  const Outer sides[2] = {{rows ? o.x : x, rows ? o.x_stride : x_stride, l->k_in, v, da, l->k_in, 1},
+                          {rows ? o.dy : dy, rows ? o.dy_stride : dy_stride, l->n_out, u, db, 1, l->rank}};
   Outer fast[2];
   int n_fast = 0;
-  for (const Outer& o : sides) {
-    if (!o.out) continue;
-    if (adapted && tensor_path(l, o.q, o.q_stride)) {
-      fast[n_fast++] = o;
+  for (const Outer& side : sides) {
+    if (!side.out) continue;
+    if (adapted && tensor_path(o, side.q, side.q_stride)) {
+      fast[n_fast++] = side;
       continue;
     }
-    outer_simple<T><<<dim3((unsigned)((o.cols + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
-        o.p, l->rank, static_cast<const T*>(o.q), o.q_stride, o.cols, offsets, ids, count, rows, l->d_alpha,
-        static_cast<T*>(o.out), l->rank * o.cols, o.sr, o.sc);
+    outer_simple<T><<<dim3((unsigned)((side.cols + 127) / 128), (l->rank + 7) / 8, l->n_adapters), 128, 0, s>>>(
+        side.p, l->rank, static_cast<const T*>(side.q), side.q_stride, side.cols, offsets, ids, count, rows,
+        l->d_alpha, static_cast<T*>(side.out), l->rank * side.cols, side.sr, side.sc);
   }
   if (n_fast) {
     const int rc = outer_tensor<T>(fast, n_fast, l->rank, l->n_adapters, q, rows, row_id,

@@ -80,7 +80,8 @@ class Case:
         dx = torch.full((self.rows, self.k), 7.0, dtype=self.dtype, device="cuda")
         da, db = torch.full_like(self.a, 7.0), torch.full_like(self.b, 7.0)
         if not self.a.shape[0]:
-            self.linear.backward(None, self.dy, None, dx=dx, requests=self.requests, status=self.status, **kw)
+            self.linear.backward(None, self.dy, None, dx=dx, requests=self.requests, workspace=self.ws,
+                                 status=self.status, **kw)
         else:
             self.linear.backward(self.x, self.dy, u, dx=dx, da=da, db=db, requests=self.requests, workspace=self.ws,
                                  status=self.status, **kw)
@@ -181,6 +182,8 @@ SIZES = [
     (5, 7, 3, 3, 2, [2, 1], [1, 0]),
     (1, 1, 1, 1, 1, [1], [0]),
     (70, 129, 130, 127, 1, [70], [0]),
+    (400, 520, 264, 20, 3, [150, 0, 250], [1, 0, 2]),
+    (150, 1000, 1001, 33, 4, [31, 64, 1, 54], [3, 0, 1, 3]),
 ]
 
 
@@ -191,10 +194,24 @@ def test_forward_and_backward_equal_the_formula(env, size, n_scale, dtype):
     Case(env, *size, dtype, n_scale, seed=size[0] + size[1]).check()
 
 
-@pytest.mark.parametrize("rows,n,k", [(1, 256, 512), (33, 272, 528), (200, 1024, 256), (515, 400, 1040), (9, 33, 17)])
+@pytest.mark.parametrize("rows,n,k", [(1, 256, 512), (33, 272, 528), (200, 1024, 256), (515, 400, 1040), (9, 33, 17),
+                                      (40, 264, 520), (300, 130, 1000)])
 def test_without_adapters(env, rows, n, k):
     for n_scale in (0, 1, "row"):
-        Case(env, rows, n, k, 1, 0, [rows], [-1], "bf16", n_scale, seed=rows).check()
+        c = Case(env, rows, n, k, 1, 0, [rows], [-1], "bf16", n_scale, seed=rows)
+        c.check()
+        # without a workspace nothing is copied: odd sizes take the plain kernels
+        y, _ = c.forward()
+        dx, _, _ = c.backward(None)
+        c.ws = None
+        want, _, size, pairs = c.exact_forward()
+        c.near(c.forward()[0], want, size, k, pairs)
+        wdx, _, _, size, pairs, _, _ = c.exact_backward(torch_zeros(c))
+        c.near(c.backward(None)[0], wdx, size, n, pairs, twice=c.n_scale > 1)
+
+
+def torch_zeros(c):
+    return c.env[1].zeros(c.rows, 1, device="cuda")
 
 
 @pytest.mark.parametrize("rows", [40, 600])
@@ -313,8 +330,9 @@ def test_strided_rows_and_views(env, rows, n, k):
         wide_x[:, shift:shift + k] = c.x
         wide_y = torch.full((rows, n + pad), 5.0, dtype=c.dtype, device="cuda")
         lin = L.Linear(wide_w[:, shift * 2:shift * 2 + k], scale=c.scale, adapters=L.Adapters(c.a, c.b, c.alpha))
+        ws = torch.zeros(lin.workspace_size(rows), dtype=torch.uint8, device="cuda")
         y = wide_y[:, shift:shift + n]
-        lin.forward(wide_x[:, shift:shift + k], y, requests=c.requests, workspace=c.ws, status=c.status)
+        lin.forward(wide_x[:, shift:shift + k], y, requests=c.requests, workspace=ws, status=c.status)
         want, _, size, pairs = c.exact_forward()
         c.near(y, want, size, k + 16, pairs)
         assert bool((wide_y[:, :shift] == 5).all()) and bool((wide_y[:, shift + n:] == 5).all())
@@ -323,7 +341,7 @@ def test_strided_rows_and_views(env, rows, n, k):
         wide_dy = torch.full((rows, n + pad), 3.0, dtype=c.dtype, device="cuda")
         wide_dy[:, shift:shift + n] = c.dy
         lin.backward(wide_x[:, shift:shift + k], wide_dy[:, shift:shift + n], u0, dx=dx, requests=c.requests,
-                     workspace=c.ws)
+                     workspace=ws)
         wdx, _, _, size, pairs, _, _ = c.exact_backward(u0)
         c.near(dx, wdx, size, n + 16, pairs, twice=True)
         assert bool((wide_dx[:, :shift] == 5).all()) and bool((wide_dx[:, shift + k:] == 5).all())
