@@ -398,7 +398,8 @@ size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows);
  * workspace.  d_workspace (16-byte aligned) belongs to the call until it ends
  * on the stream.  Strides count elements.  Asynchronous on stream s; errors
  * are returned before anything is enqueued: ECF8_ERR_ARG (null or bad sizes),
- * ECF8_ERR_ALIGN, ECF8_ERR_WORKSPACE, ECF8_ERR_CUDA. */
+ * ECF8_ERR_ALIGN, ECF8_ERR_WORKSPACE; ECF8_ERR_UNSUPPORTED (more than 2^21
+ * rows in tiles of 32) and ECF8_ERR_CUDA may come after a first kernel. */
 int ecf8_linear_forward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,
                         void* d_y, uint64_t y_stride, uint64_t rows, float* d_u, void* d_workspace,
                         size_t workspace_bytes, int32_t* d_status, cudaStream_t s);
@@ -434,8 +435,10 @@ typedef struct ecf8_grad {
 size_t ecf8_grad_table_bytes(int count);
 
 /* Fill h_table (host, ecf8_grad_table_bytes(count) bytes) for these tensors.
- * The set is fixed by it: pointers, sizes and types.  ECF8_ERR_ARG,
- * ECF8_ERR_ALIGN. */
+ * The set is fixed by it: pointers, sizes and types.  ECF8_ERR_ARG (also where
+ * an output shares memory with another output or another tensor's input, as
+ * a tensor that is listed twice in place does), ECF8_ERR_ALIGN,
+ * ECF8_ERR_CAPACITY (no host memory for that check). */
 int ecf8_grad_build_table(const ecf8_grad* grads, int count, void* h_table);
 
 /* Bytes of device workspace a norm or clip call needs. */

@@ -555,6 +555,17 @@ def _rows(t, what: str, dtype, rows: int, cols: int) -> int:
     return stride if rows > 1 else max(stride, cols)
 
 
+def _here(what: str, device, tensors) -> None:
+    """Every tensor on this CUDA device, which is the current one: the kernels
+    run there, and reach no other device's memory."""
+    import torch
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
+        _refuse(what, f"tensors are on {device}, which is not the current CUDA device")
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.device != device:
+            _refuse(what, f"tensors on {device} and {t.device}")
+
+
 @dataclass
 class Adapters:
     """Low-rank adapters of one projection: a (count, rank, in), b (count,
@@ -637,6 +648,10 @@ class Linear:
         self.n_out, self.k_in, self.dtype = int(n), int(k), dtype
         self._keep, self._d, self._ref = (weight, scale, adapters), d, ctypes.byref(d)
         self._f32, self._i32 = torch.float32, torch.int32
+        self._own = [t for t in (weight, scale, *((adapters.a, adapters.b, adapters.alpha) if self.rank else ()))
+                     if t is not None and not isinstance(t, int)]
+        if any(t.device != self._own[0].device for t in self._own):
+            _refuse("Linear", f"tensors on {[str(t.device) for t in self._own]}")
 
     def workspace_size(self, rows: int) -> int:
         """Bytes of device workspace forward and backward need for this many rows."""
@@ -660,7 +675,11 @@ class Linear:
         ys = _rows(y, "Linear y", self.dtype, rows, self.n_out)
         if u is not None:
             _is(u, "Linear u", self._f32, (rows, self.rank))
-        _check(_lib.ecf8_linear_forward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(y), ys, rows, _ptr(u),
+        q = self._requests(requests)
+        _here("Linear forward", x.device, (y, u, workspace, status, *self._own[:1]))
+        if requests is not None:
+            _here("Linear forward", x.device, (requests.offsets, requests.ids))
+        _check(_lib.ecf8_linear_forward(self._ref, q, _ptr(x), xs, _ptr(y), ys, rows, _ptr(u),
                                         _ptr(workspace), _nbytes(workspace, 0), _ptr(status), _stream(stream)),
                "ecf8_linear_forward")
 
@@ -680,7 +699,11 @@ class Linear:
                 if not self.rank:
                     _refuse(what, "there are no adapters")
                 _is(g, what, self.dtype, getattr(self._keep[2], of).shape)
-        _check(_lib.ecf8_linear_backward(self._ref, self._requests(requests), _ptr(x), xs, _ptr(dy), ds, _ptr(u),
+        q = self._requests(requests)
+        _here("Linear backward", dy.device, (x, u, dx, da, db, workspace, status, *self._own[:1]))
+        if requests is not None:
+            _here("Linear backward", dy.device, (requests.offsets, requests.ids))
+        _check(_lib.ecf8_linear_backward(self._ref, q, _ptr(x), xs, _ptr(dy), ds, _ptr(u),
                                          _ptr(dx), gs, _ptr(da), _ptr(db), rows, _ptr(workspace),
                                          _nbytes(workspace, 0), _ptr(status), _stream(stream)),
                "ecf8_linear_backward")
@@ -722,20 +745,29 @@ class GradSet:
             arr[i] = Grad(_ptr(g), _ptr(o), g.numel(), _dtype_of(g, f"GradSet tensor {i}"))
         self._h = np.zeros(int(_lib.ecf8_grad_table_bytes(len(grads))), dtype=np.uint8)
         _check(_lib.ecf8_grad_build_table(arr, len(grads), self._h.ctypes.data), "ecf8_grad_build_table")
-        dev = grads[0].device if grads else torch.device("cuda")
+        dev = grads[0].device if grads else torch.device("cuda", torch._C._cuda_getDevice())
+        _here("GradSet", dev, (*grads, *outs))
+        self._device = dev
         self._d = torch.from_numpy(self._h).to(dev)
         self._ws = torch.empty(int(_lib.ecf8_grad_workspace_size()), dtype=torch.uint8, device=dev)
         self._keep = (grads, outs)
         self._args = (self._h.ctypes.data, _ptr(self._d))
         self._ws_args = (_ptr(self._ws), self._ws.numel())
 
+    def _one(self, norm, status) -> None:
+        if str(norm.dtype) != "torch.float32" or norm.numel() != 1:
+            _refuse("GradSet norm", f"want one float32, got {norm.dtype} {tuple(norm.shape)}")
+        _here("GradSet", self._device, (norm, status))
+
     def norm(self, norm, status=None, stream=None) -> None:
         """Asynchronously writes the L2 norm of the whole set to ``norm`` (one float32)."""
+        self._one(norm, status)
         _check(_lib.ecf8_grad_norm(*self._args, _ptr(norm), *self._ws_args, _ptr(status), _stream(stream)),
                "ecf8_grad_norm")
 
     def clip(self, max_norm: float, norm, status=None, stream=None) -> None:
         """``norm``, then every tensor times min(1, max_norm / (norm + 1e-6)).
         A norm that is not finite sets ECF8_STATUS_NONFINITE and changes no value."""
+        self._one(norm, status)
         _check(_lib.ecf8_grad_clip(*self._args, float(max_norm), _ptr(norm), *self._ws_args, _ptr(status),
                                    _stream(stream)), "ecf8_grad_clip")

@@ -26,6 +26,9 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <vector>
+
 #include "ecf8.h"
 
 namespace {
@@ -258,6 +261,31 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const Header* table, uin
   });
 }
 
+struct Span {
+  uintptr_t from, to;
+  int tensor;
+};
+
+// Whether any output shares bytes with another output, or with an input other than its own in place.
+bool outputs_collide(const ecf8_grad* grads, int count) {
+  std::vector<Span> outs;
+  for (int i = 0; i < count; ++i)
+    if (grads[i].n && grads[i].d_out)
+      outs.push_back(Span{(uintptr_t)grads[i].d_out, (uintptr_t)grads[i].d_out + grads[i].n * width(grads[i].dtype), i});
+  std::sort(outs.begin(), outs.end(), [](const Span& a, const Span& b) { return a.from < b.from; });
+  for (size_t i = 1; i < outs.size(); ++i)
+    if (outs[i].from < outs[i - 1].to) return true;
+  for (int i = 0; i < count; ++i) {
+    if (!grads[i].n) continue;
+    const uintptr_t from = (uintptr_t)grads[i].d_in, to = from + grads[i].n * width(grads[i].dtype);
+    // the outputs do not overlap, so their ends are in order too: the first that ends past `from`
+    auto o = std::upper_bound(outs.begin(), outs.end(), from, [](uintptr_t f, const Span& s) { return f < s.to; });
+    for (; o != outs.end() && o->from < to; ++o)
+      if (o->tensor != i || o->from != from) return true;
+  }
+  return false;
+}
+
 int run(const void* h_table, const void* d_table, int clip, float max_norm, float* d_norm, void* ws, size_t ws_bytes,
         int32_t* d_status, cudaStream_t s) {
   if (!h_table || !d_table || !d_norm) return ECF8_ERR_ARG;
@@ -309,6 +337,11 @@ int ecf8_grad_build_table(const ecf8_grad* grads, int count, void* h_table) {
     if (g.n > (UINT64_MAX >> 8)) return ECF8_ERR_ARG;
     if (g.n && !g.d_in) return ECF8_ERR_ARG;
     if (((uintptr_t)g.d_in | (uintptr_t)g.d_out) & (width(g.dtype) - 1)) return ECF8_ERR_ALIGN;
+  }
+  try {
+    if (outputs_collide(grads, count)) return ECF8_ERR_ARG;
+  } catch (...) {  // no host memory for the check
+    return ECF8_ERR_CAPACITY;
   }
   Header* h = static_cast<Header*>(h_table);
   Entry* e = reinterpret_cast<Entry*>(h + 1);

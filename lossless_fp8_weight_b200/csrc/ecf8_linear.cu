@@ -445,16 +445,21 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   if (P == 2) {
     // the other CTA's barriers are ready before anything arrives on them
     cluster_sync();
-    if (a.rank) {
-      wait_predecessor();
-      if (threadIdx.x < 256) ids[threadIdx.x] = threadIdx.x < a.bt && t0 + threadIdx.x < a.rows ? a.row_id[t0 + threadIdx.x] : -1;
-      __syncthreads();
-      distinct(ids, a.bt, runs, list, &count_s, warp_sum);
-      units = count_s * ((a.rank + 15) / 16);
-      const uint32_t all = (units + 1) / 2;  // steps of two units, dealt out to the parts
-      adapter_steps = all / a.split + (part < all % a.split ? 1 : 0);
-    }
   }
+  // P = 2, by all threads between the weights' steps and the adapters': what the kernel before this one has written is
+  // not needed earlier.
+  auto find_adapters = [&] {
+    if (P != 2 || !a.rank) return;
+    __syncwarp();
+    wait_predecessor();
+    if (threadIdx.x < 256)
+      ids[threadIdx.x] = threadIdx.x < a.bt && t0 + threadIdx.x < a.rows ? a.row_id[t0 + threadIdx.x] : -1;
+    __syncthreads();
+    distinct(ids, a.bt, runs, list, &count_s, warp_sum);
+    units = count_s * ((a.rank + 15) / 16);
+    const uint32_t all = (units + 1) / 2;  // steps of two units, dealt out to the parts
+    adapter_steps = all / a.split + (part < all % a.split ? 1 : 0);
+  };
 
   if (warp == 0) {
     if (elect_one()) {
@@ -482,8 +487,11 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (++s == a.stages) s = 0, turn ^= 1;
     }
     if (!ok) drain(full, s, turn, a.stages);
+    find_adapters();
   } else if (warp == 1) {
-    if (side == 0) {
+    if (side != 0) {
+      find_adapters();
+    } else {
       const uint32_t mask = 3u << leader;
       const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128 * P, a.bt);
       uint32_t g = 0, s = 0, turn = 0;  // 64-wide steps, stage, parity
@@ -507,6 +515,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         }
         if (++s == a.stages) s = 0, turn ^= 1;
       }
+      find_adapters();
       if (P == 2) {
         const uint32_t idesc_pair = idesc_f16(true, 128 * P, a.bt);
         for (uint32_t i = 0; i < adapter_steps && ok; ++i, ++g) {
@@ -638,6 +647,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (s >= a.stages) s -= a.stages, turn ^= 1;
     }
 
+    find_adapters();
     if (P == 2) {
       // Adapter steps go on in the ring of stages: a thread widens two units' factors of its column into the slot, and
       // writes its rows' side of both where the stage's rows were.  What they read is fetched before the wait.
@@ -1540,8 +1550,12 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.rows = rows;
   a.cols = cols;
   a.len = len;
-  a.bt = rows >= 256 ? 256 : (uint32_t)((rows + 15) / 16 * 16);
-  const bool pair = a.bt > 128;  // two CTAs to a tile; else two CTAs to an SM
+  // Two CTAs to a tile of 256 columns where such tiles occupy half of the SMs at least; else single ones, two to an SM,
+  // on tiles of at most 128 rows, which give more CTAs before the reduction has to be split (256 rows of 1024x4096
+  // backward: 29 us in pairs, 16 us so; 200 rows of 4096x4096: 33 and 21).
+  const bool pair = rows > 128 && (cols + 255) / 256 * ((rows + 255) / 256) >= 37;
+  const uint64_t tall = pair ? 256 : 128;
+  a.bt = (uint32_t)(rows >= tall ? tall : (rows + 15) / 16 * 16);
   const int kb = pair ? 1 : 2, width = pair ? 2 : 1;
   a.blocks = (uint32_t)((len + 64 * kb - 1) / (64 * kb));
   const uint64_t tiles = (cols + 128 * width - 1) / (128 * width), row_tiles = (rows + a.bt - 1) / a.bt;

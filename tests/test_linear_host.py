@@ -164,9 +164,34 @@ def test_gradient_tables_are_checked(L):
     assert L._lib.ecf8_grad_table_bytes(-1) == 0
 
 
+def test_outputs_of_a_set_may_not_share_memory(L):
+    far = FAKE + (1 << 16)
+    assert _grads(L, [(FAKE, FAKE, 10, 0), (FAKE, FAKE, 10, 0)])[0] == ARG        # listed twice, in place
+    assert _grads(L, [(FAKE, far, 10, 0), (FAKE, far + 18, 10, 0)])[0] == ARG     # outputs overlap by a value
+    assert _grads(L, [(FAKE, far, 10, 0), (FAKE, far + 20, 10, 0)])[0] == 0       # and lie next to each other
+    assert _grads(L, [(FAKE, far, 10, 0), (far + 18, 0, 10, 0)])[0] == ARG        # an output over another's input
+    assert _grads(L, [(FAKE, FAKE + 2, 10, 0)])[0] == ARG                         # shifted in place
+    assert _grads(L, [(FAKE, 0, 10, 0), (FAKE, 0, 10, 0), (FAKE + 4, 0, 3, 2)])[0] == 0  # inputs may: norm only
+    many = [(FAKE + 64 * i, FAKE + 64 * i, 16, 2) for i in range(300)]
+    assert _grads(L, many)[0] == 0
+    assert _grads(L, many + [(FAKE + 64 * 299, far + (1 << 20), 17, 2)])[0] == ARG  # reads what another writes
+
+
+def test_tensors_off_the_gpu_are_refused(L):
+    import torch
+    w = torch.zeros(64, 96, dtype=torch.uint8)
+    x, y = torch.zeros(5, 96, dtype=torch.bfloat16), torch.zeros(5, 64, dtype=torch.bfloat16)
+    lin = L.Linear(w)
+    for call in (lambda: lin.forward(x, y, stream=0), lambda: lin.backward(None, y, None, dx=x, stream=0),
+                 lambda: L.GradSet([x])):
+        with pytest.raises(L.Ecf8Error) as e:
+            call()
+        assert e.value.code == ARG
+
+
 def test_gradient_calls_are_checked(L):
     _, table = _grads(L, [(FAKE, FAKE, 10, 0)])
-    _, half = _grads(L, [(FAKE, FAKE, 10, 0), (FAKE, 0, 10, 0)])
+    _, half = _grads(L, [(FAKE, FAKE, 10, 0), (FAKE + 64, 0, 10, 0)])
     h, ws = table.ctypes.data, L._lib.ecf8_grad_workspace_size()
 
     def clip(h=h, d=FAKE, most=1.0, norm=FAKE, w=FAKE, ws_bytes=ws, status=0):
