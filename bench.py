@@ -463,6 +463,47 @@ _LAYER_SHAPES = {"q_proj": (4096, 4096), "k_proj": (1024, 4096), "v_proj": (1024
                  "gate_proj": (14336, 4096), "up_proj": (14336, 4096), "down_proj": (4096, 14336)}
 
 
+def linear_pass(torch, L, dev, recs, outs, ref, layers, slots, slot_bytes, n_layers, M, cap, status, compute, decode,
+                reps, timed, results):
+    """ms per layer of a stack's 7 projections by L.Linear: on resident
+    weights, and from the pipeline's slots; both give the same outputs."""
+    g = torch.Generator(device=dev).manual_seed(7)
+    scale = torch.full((1,), 1.0 / 448, dtype=torch.float32, device=dev)
+    xb = {k: torch.randn(M, k, generator=g, device=dev).to(torch.bfloat16) for k in {s[1] for s in _LAYER_SHAPES.values()}}
+    ys = {r["name"]: torch.empty(M, _LAYER_SHAPES[r["name"]][0], dtype=torch.bfloat16, device=dev) for r in recs}
+    lins = {t.data_ptr(): [L.Linear(t.data_ptr() + off, shape=_LAYER_SHAPES[r["name"]], scale=scale)
+                           for r, off in zip(recs, outs)] for t in (ref, *slots)}
+
+    def project(at, stream=None):
+        for r, lin in zip(recs, lins[at]):
+            lin.forward(xb[lin.k_in], ys[r["name"]], status=status, stream=stream)
+
+    results["linear_only"] = timed(lambda: [project(ref.data_ptr()) for _ in range(n_layers)])
+    want = {k: v.clone() for k, v in ys.items()}
+    P = L.Pipeline(layers, slots, slot_bytes, depth=1, max_ctas=cap, status=status, decode_stream=decode)
+
+    def one_pass():
+        for l in range(n_layers):
+            project(P.acquire(l, compute), compute)
+            P.release(l, compute)
+
+    for y in ys.values():
+        y.zero_()
+    torch.cuda.synchronize()
+    one_pass()
+    torch.cuda.synchronize()
+    assert all(torch.equal(ys[k], want[k]) for k in want)
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record(compute)
+    for _ in range(reps):
+        one_pass()
+    e1.record(compute)
+    torch.cuda.synchronize()
+    results["linear_pipelined"] = e0.elapsed_time(e1) / reps / n_layers
+    P.close()
+    assert int(status.item()) == 0
+
+
 def run_pipeline(args):
     """Decode-on-use (ECF8 walkthrough §3.2.2; DFloat11 article §4): a stack
     of Llama-3-8B layers whose FP8 GEMMs (y = x W^T for all 7 projections, M
@@ -567,6 +608,9 @@ def run_pipeline(args):
         results[f"pipelined_ctas{cap}"] = e0.elapsed_time(e1) / reps / n_layers
         P.close()
     assert int(status.item()) == 0
+    # the same stack through the library's own projections: BF16 activations, weights read from the slots
+    linear_pass(torch, L, dev, recs, outs, ref, layers, slots, slot_bytes, n_layers, M, args.pipeline_ctas[0], status,
+                compute, decode, reps, timed, results)
     best = min(v for k, v in results.items() if k.startswith("pipelined"))
     hidden = (results["serial"] - best) / max(1e-9, results["serial"] - results["gemm_only"])
     line = {"workload": f"pipeline_llama3_8b_x{n_layers}_tokens{M}", "metric": "ms per layer",

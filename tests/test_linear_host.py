@@ -153,7 +153,7 @@ def _grads(L, entries):
 
 
 def test_gradient_tables_are_checked(L):
-    assert _grads(L, [(FAKE, FAKE, 10, 0), (0, 0, 0, 2), (FAKE + 2, 0, 1, 1)])[0] == 0
+    assert _grads(L, [(FAKE, FAKE, 10, 0), (0, 0, 0, 2), (FAKE + 66, 0, 1, 1)])[0] == 0
     assert _grads(L, [(FAKE, FAKE, 10, 3)])[0] == ARG
     assert _grads(L, [(0, FAKE, 10, 0)])[0] == ARG
     assert _grads(L, [(FAKE, FAKE, 1 << 60, 0)])[0] == ARG
