@@ -183,6 +183,10 @@ SIZES = [
     (1, 1, 1, 1, 1, [1], [0]),
     (70, 129, 130, 127, 1, [70], [0]),
     (400, 520, 264, 20, 3, [150, 0, 250], [1, 0, 2]),
+    # more tiles than pairs of SMs
+    (1777, 4096, 1056, 24, 3, [700, 900, 100], [1, 2, 0]),
+    (1280, 4608, 1024, 8, 2, [1270], [1]),
+    (1250, 4096, 1552, 40, 2, [620, 1, 600], [0, 1, 1]),
     (150, 1000, 1001, 33, 4, [31, 64, 1, 54], [3, 0, 1, 3]),
 ]
 
