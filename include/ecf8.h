@@ -398,8 +398,8 @@ size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows);
  * workspace.  d_workspace (16-byte aligned) belongs to the call until it ends
  * on the stream.  Strides count elements.  Asynchronous on stream s; errors
  * are returned before anything is enqueued: ECF8_ERR_ARG (null or bad sizes),
- * ECF8_ERR_ALIGN, ECF8_ERR_WORKSPACE; ECF8_ERR_UNSUPPORTED (more than 2^21
- * rows in tiles of 32) and ECF8_ERR_CUDA may come after a first kernel. */
+ * ECF8_ERR_ALIGN, ECF8_ERR_WORKSPACE; ECF8_ERR_UNSUPPORTED (more than
+ * 65535 tiles of 256 rows) and ECF8_ERR_CUDA may come after a first kernel. */
 int ecf8_linear_forward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,
                         void* d_y, uint64_t y_stride, uint64_t rows, float* d_u, void* d_workspace,
                         size_t workspace_bytes, int32_t* d_status, cudaStream_t s);
