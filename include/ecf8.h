@@ -413,7 +413,9 @@ int ecf8_linear_forward(const ecf8_linear* lin, const ecf8_requests* requests, c
  * adapters that no row uses; an adapter's rows are summed over all its
  * requests, in an order that does not vary.  d_u is the forward call's (read
  * for db only), d_x is read for da only.  With one scale per output row the
- * tensor-core path rounds s * W to the activation type before the product. */
+ * tensor-core path takes s * W as a value of the activation type and its rest:
+ * of a term, BF16 loses 2^-17, FP16 2^-23 or, if that is more, 2^-31 of what
+ * the largest scale in its place would give. */
 int ecf8_linear_backward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,
                          const void* d_dy, uint64_t dy_stride, const float* d_u, void* d_dx, uint64_t dx_stride,
                          void* d_da, void* d_db, uint64_t rows, void* d_workspace, size_t workspace_bytes,

@@ -184,6 +184,12 @@ __global__ void __launch_bounds__(256) product_simple(const T* q, uint64_t q_str
 // not finite are left out of it and their terms added one by one at the end,
 // where they meet their own rows only and no rest; so are columns whose scale
 // is zero or extreme.
+//
+// The input gradient with a scale for every output row needs s W, which no
+// 16-bit type holds: it enters as a 16-bit value and a 16-bit rest, two
+// products a step (one of them alone made the error up to 1.3 times that of
+// the final rounding).  2^-17 of a term is lost in BF16; in FP16 2^-23, or 2^-31
+// of the largest scale's where that is more.
 
 template <class T> struct Widen;
 template <> struct Widen<__nv_bfloat16> {
@@ -405,8 +411,12 @@ template <class T, int P, int KB, int G, int BACK>
 __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     product_tc(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_q,
                const __grid_constant__ ProductArgs a) {
-  // widened steps in tensor memory: as many as there are stages, which they then follow, or four
-  constexpr uint32_t slots = P == 2 ? 8 : 4, columns = P == 2 ? 512 : 256;
+  // widened steps in tensor memory: as many as there are stages, which they then follow, or four; half of that where
+  // a step has two parts
+  constexpr uint32_t most_slots = P == 2 ? kSlots : 4, columns = P == 2 ? 512 : 256;
+  const bool wide = BACK && a.n_scale > 1;
+  const uint32_t slot_bits = (P == 2 ? 3 : 2) - (wide ? 1 : 0), slot_mask = (1u << slot_bits) - 1;
+  const uint32_t slot_columns = wide ? 64 : 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
   __shared__ uint32_t tmem_base;
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
-    for (uint32_t i = 0; i < slots; ++i) {
+    for (uint32_t i = 0; i < most_slots; ++i) {
       mbar_init(ready + 8 * i, 4 * P);
       mbar_init(freed + 8 * i, 1);
     }
@@ -454,7 +464,9 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = tmem_base, tmem_a = tmem + (columns - slots * 32);
+  const uint32_t tmem = tmem_base, tmem_a = tmem + (columns - most_slots * 32);
+  // where a step is widened to: `at` is its stage with P = 2, its slot else
+  auto widened = [&](uint32_t at) { return tmem_a + (at & slot_mask) * slot_columns; };
   uint32_t adapter_steps = 0, units = 0;
   if (P == 2) {
     // the other CTA's barriers are ready before anything arrives on them
@@ -514,14 +526,17 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
 #pragma unroll
         for (int k = 0; k < KB && ok; ++k, ++g) {
           // the warps that report a step ready have waited for their CTA's tiles
-          const uint32_t slot = P == 2 ? s : g % slots;
-          ok = mbar_wait<P == 2>(ready + 8 * slot, P == 2 ? turn : g / slots & 1, failed);
+          const uint32_t slot = P == 2 ? s : g & slot_mask;
+          ok = mbar_wait<P == 2>(ready + 8 * slot, P == 2 ? turn : g >> slot_bits & 1, failed);
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * rows_here * 128);
           if (elect_one()) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, tmem_a + slot * 32 + m * 8, b + m * 2, idesc, g > 0 || m > 0);
+            for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, widened(slot) + m * 8, b + m * 2, idesc, g > 0 || m > 0);
+            if (wide)
+#pragma unroll
+              for (int m = 0; m < 4; ++m) mma_ts<P>(tmem, widened(slot) + 32 + m * 8, b + m * 2, idesc, 1);
             if (P == 1) mma_commit<P>(freed + 8 * slot, mask);
             if (k == KB - 1) mma_commit<P>(empty + 8 * s, mask);
           }
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           const uint32_t first = (i * a.split + part) * 2;
           if (elect_one()) {
             for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
-              const uint32_t hi = tmem_a + s * 32 + u * 16;
+              const uint32_t hi = widened(s) + u * 16;
               mma_ts<P>(tmem, hi, b + u * 4, idesc_pair, g > 0 || u > 0);
               mma_ts<P>(tmem, hi, b + u * 4 + 2, idesc_pair, 1);
               mma_ts<P>(tmem, hi + 8, b + u * 4, idesc_pair, 1);
@@ -558,10 +573,10 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     const int w4 = warp - 2, quarter = warp % 4, group = w4 / 4;
     const uint32_t row = quarter * 32 + lane;
     const uint64_t c = c0 + row;
-    // with a scale for each term of the reduction the weights are scaled here, by powers of two that keep FP16 in range
-    const bool scaled = BACK && a.n_scale > 1;
+    // With a scale for each term of the reduction the weights are scaled here, FP16 by a power of two more that brings
+    // the largest scale to [64, 128): the largest product, 57344, is in range.
     float unit = 1.0f;
-    if (scaled && !Widen<T>::kBf16) {
+    if (wide && !Widen<T>::kBf16) {
       float m = 0;
       for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += 128 * G) {
         const float s = fabsf(a.scale[i]);
@@ -571,8 +586,8 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (lane == 0) max_s[w4] = m;
       asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");
       for (int i = 0; i < 4 * G; ++i) m = fmaxf(m, max_s[i]);
-      const uint32_t e = __float_as_uint(m) >> 23;  // unit = 2^-floor(log2 m), so that m * unit is in [1, 2)
-      if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23);
+      const uint32_t e = __float_as_uint(m) >> 23;  // m is in [2^(e-127), 2^(e-126))
+      unit = __uint_as_float((e > 6 ? 260 - e : 254) << 23);
       if (threadIdx.x == 64) unit_s = unit;
     }
     // the output's scale, and whether the adapters' factors may be divided by it
@@ -591,12 +606,19 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       }
     };
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    // P = 2: waits until the products of the stage's last use have ended, and where a step takes two slots' columns, those
+    // of the group's last step, which lie in them and are later ones.
+    static_assert(P == 1 || (kSlots == 8 && G == 4), "a group's last step is four stages back in a ring of eight");
+    auto wait_free = [&](uint32_t s, uint32_t turn) {
+      return wide ? mbar_wait_warp(empty + 8 * (s ^ 4), s >= 4 ? turn : turn ^ 1, failed)
+                  : mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
+    };
     bool ok = true;
     uint32_t g = group, s = group / KB, turn = 0;
     while (s >= a.stages) s -= a.stages, turn ^= 1;
     for (; g < steps; g += G) {
-      const uint32_t k = g % KB, at = base + s * stage_bytes, slot = P == 2 ? s : g % slots;
-      if (scaled) {
+      const uint32_t k = g % KB, at = base + s * stage_bytes, slot = P == 2 ? s : g & slot_mask;
+      if (wide) {
         // past the last term the scale is not read; the weights there are zeros
         const uint64_t j = (uint64_t)b0 * 64 * KB + (uint64_t)g * 64 + lane;
         const float x = j < a.n_scale ? a.scale[j] * unit : 0.0f, y = j + 32 < a.n_scale ? a.scale[j + 32] * unit : 0.0f;
@@ -608,11 +630,13 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       // A group skips the stage's uses by the others, and a barrier tells its phases apart by their parity alone: the
       // stage's last products have ended (which no phase can overtake, as this step is still to come), then its
       // load is the one waited for.
-      ok = (P == 1 || mbar_wait_warp(empty + 8 * s, turn ^ 1, failed)) && mbar_wait_warp(full + 8 * s, turn, failed);
+      ok = (P == 1 || wait_free(s, turn)) && mbar_wait_warp(full + 8 * s, turn, failed);
+      // P = 2: the stage was loaded after its last products ended, and with them the slot's
+      if (P == 1) ok = ok && mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed);
       if (!ok) break;
-      uint32_t v[32];
+      fence_after();
       if (!BACK) {
-        uint32_t b[16];
+        uint32_t b[16], v[32];
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const uint32_t chunk = k * 4 + h;
@@ -627,15 +651,15 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           v[2 * q] = widen2<T>(b[q]);
           v[2 * q + 1] = widen2<T>(b[q] >> 16);
         }
+        tmem_st32(widened(slot) + lanes, v);
       } else {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
-          uint32_t* w = v + 16 * half;
-          uint32_t b[32];
+          uint32_t b[32], w[16], rest[16];
 #pragma unroll
           for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
-          if (!scaled) {
+          if (!wide) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = widen2<T>(b[2 * j + 1] * 256u + b[2 * j]);
           } else {
@@ -644,17 +668,14 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
               const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w4 : 0][32 * half + 2 * j]);
               const float2 y = widen2_float(b[2 * j + 1] * 256u + b[2 * j]),
                            z = widen2_float(b[2 * j + 3] * 256u + b[2 * j + 2]);
-              w[j] = Widen<T>::pack(y.x * x.x, y.y * x.y);
-              w[j + 1] = Widen<T>::pack(z.x * x.z, z.y * x.w);
+              split_pair<T>(y.x * x.x, y.y * x.y, w[j], rest[j]);
+              split_pair<T>(z.x * x.z, z.y * x.w, w[j + 1], rest[j + 1]);
             }
+            tmem_st16(widened(slot) + 32 + half * 16 + lanes, rest);
           }
+          tmem_st16(widened(slot) + half * 16 + lanes, w);
         }
       }
-      // P = 2: the stage was loaded after its last products ended, and with them the slot's
-      if (P == 1) ok = mbar_wait_warp(freed + 8 * slot, (g / slots & 1) ^ 1, failed);
-      if (!ok) break;
-      fence_after();
-      tmem_st32(tmem_a + slot * 32 + lanes, v);
       announce(slot);
       if (KB == 1 || G >= KB) s += G / KB;
       else if (k == KB - 1) ++s;
@@ -697,7 +718,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
             }
           }
           if (!waited) {
-            ok = mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
+            ok = wait_free(s, turn);
             waited = true;
           }
           if (ok && t < rows_here)
@@ -711,7 +732,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         }
         if (!ok) break;
         fence_after();
-        tmem_st32(tmem_a + s * 32 + lanes, v);
+        tmem_st32(widened(s) + lanes, v);
         fence_async();
         announce(s);
         s += G;
