@@ -904,17 +904,33 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   __syncthreads();
   // the requests that reach into this tile write their rows' ids
+  bool backwards = false;
   for (uint32_t i = threadIdx.x; i < a.count; i += kShrinkThreads) {
     const int32_t b = a.offsets[i], e = a.offsets[i + 1], id = a.request_ids[i];
     const bool known = id < 0 || (uint32_t)id < a.n_adapters;
     if (b < 0 || e < b || (int64_t)e > (int64_t)a.rows || !known) {
       if (a.status && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, ECF8_STATUS_BAD_REQUEST);
     }
+    backwards |= e < b;
     if (id < 0 || !known) continue;
     const int64_t lo = max((int64_t)b - (int64_t)t0, (int64_t)0), hi = min((int64_t)e - (int64_t)t0, (int64_t)n);
     for (int64_t t = lo; t < hi; ++t) ids[t] = id;
   }
-  __syncthreads();
+  if (__syncthreads_or(backwards)) {
+    // Requests of such a table may overlap, and their threads have written shared rows in any order.  The CTAs of a
+    // cluster have to agree on every row, since they share its sums and leave together: the last request takes it.
+    if (threadIdx.x < 256) ids[threadIdx.x] = -1;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < a.count; i += kShrinkThreads) {
+      const int32_t b = a.offsets[i], e = a.offsets[i + 1], id = a.request_ids[i];
+      if (id < 0 || (uint32_t)id >= a.n_adapters) continue;
+      const int64_t lo = max((int64_t)b - (int64_t)t0, (int64_t)0), hi = min((int64_t)e - (int64_t)t0, (int64_t)n);
+      for (int64_t t = lo; t < hi; ++t) atomicMax(&ids[t], (int32_t)i);
+    }
+    __syncthreads();
+    if (threadIdx.x < 256 && ids[threadIdx.x] >= 0) ids[threadIdx.x] = a.request_ids[ids[threadIdx.x]];
+    __syncthreads();
+  }
   if (chunk == 0 && crank == 0 && threadIdx.x < n) a.row_id[t0 + threadIdx.x] = ids[threadIdx.x];
   distinct(ids, n, runs, list, &count_s, warp_sum);
   // rows without an adapter have zeros

@@ -27,3 +27,31 @@ def test_a_scaled_weight_is_not_rounded_before_the_product(env, rows, k, dtype):
         most += 2.0 ** -31 * float(s.max()) * c.dy.double().diag()[:, None]
     err = (dx.double() - want).abs()
     assert bool((err <= most).all()), float((err / most).max())
+
+
+@pytest.mark.parametrize("rows,n,k,rank", [(64, 256, 4096, 128), (64, 144, 2048, 16), (300, 272, 512, 96)])
+def test_requests_that_overlap_leave_the_other_rows(env, rows, n, k, rank):
+    """Offsets that go back and forth, each request with an adapter of its own: rows of one request only are as they
+    should be, the others get the same values in every call, and the status tells."""
+    L, torch = env
+    # rows 0-7 and 40- belong to one request; 8-39 to up to four
+    ends = [v for i in range(11) for v in (8 + 2 * i, 16 + 2 * i)]
+    offsets = [0, *ends, 40, rows]
+    c = Case(env, rows, n, k, rank, len(offsets) - 1, [1] * (len(offsets) - 1), range(len(offsets) - 1), "bf16", 1,
+             seed=31)
+    c.requests.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+    y, u = c.forward()
+    assert int(c.status.item()) == L.STATUS_BAD_REQUEST
+    grads = c.backward(u)
+    for _ in range(5):
+        y2, u2 = c.forward()
+        assert torch.equal(y, y2) and torch.equal(u, u2)
+        assert all(torch.equal(p, q) for p, q in zip(grads, c.backward(u)))
+    # the formula for the rows of one request
+    c.offsets, c.ids = [0, 8, 40, rows], [0, -1, len(offsets) - 2]
+    want, wu, size, pairs = c.exact_forward()
+    wdx, _, _, sizex, pairsx, _, _ = c.exact_backward(u)
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[8:40] = False
+    c.near(y[keep], want[keep], size[keep], k + rank, pairs[keep])
+    c.near(grads[0][keep], wdx[keep], sizex[keep], n + rank, pairsx[keep])
