@@ -887,8 +887,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   const uint32_t pad = (a.rank + 7) / 8 * 8;
 
   const uint32_t n = (uint32_t)(a.rows - t0 < a.bt ? a.rows - t0 : a.bt);
-  start_successor();
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 64) {
     tma_prefetch(&map_f);
     tma_prefetch(&map_q);
   }
@@ -902,7 +901,17 @@ __global__ void __launch_bounds__(kShrinkThreads)
     failed_s = 0;
     mbar_init_fence();
   }
+  if (warp == 1) {
+    tmem_alloc<1>(smem_addr(&tmem_base), columns);
+    tmem_release_permit<1>();
+  }
+  fence_before();
   __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base;
+  // Only now: the projection's CTAs hold their tensor memory until this kernel has ended.  Were one to take an SM's while
+  // a CTA here still waited for some, neither would go on.
+  start_successor();
   // the requests that reach into this tile write their rows' ids
   bool backwards = false;
   for (uint32_t i = threadIdx.x; i < a.count; i += kShrinkThreads) {
@@ -939,16 +948,11 @@ __global__ void __launch_bounds__(kShrinkThreads)
       if (ids[t] < 0)
         for (uint32_t r = lane; r < a.rank; r += 32) a.p[(t0 + t) * a.rank + r] = 0.0f;
   const uint32_t first = chunk * a.per;
-  if (first >= count_s) return;  // the same in every CTA of the cluster
-  const uint32_t mine = count_s - first < a.per ? count_s - first : a.per;
-  if (warp == 1) {
-    tmem_alloc<1>(smem_addr(&tmem_base), columns);
-    tmem_release_permit<1>();
+  if (first >= count_s) {  // the same in every CTA of the cluster
+    if (warp == 1) tmem_free<1>(tmem, columns);
+    return;
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t mine = count_s - first < a.per ? count_s - first : a.per;
 
   if (warp == 0) {
     uint32_t s = 0, turn = 0;  // stage, and the parity of its use
