@@ -72,6 +72,16 @@ __device__ inline void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) 
   lo = Widen<T>::pack(isfinite(h.x) ? x - h.x : 0.0f, isfinite(h.y) ? y - h.y : 0.0f);
 }
 
+// The same for scaled weights, with fewer instructions: a rest that is no number (of an infinity) becomes -L, which adds
+// nothing to what an infinity makes of a sum.  L is above every rest of FP16 weights, 2^4, and of BF16 weights to 2^68.
+template <class T>
+__device__ inline void split_scaled(float x, float y, uint32_t& hi, uint32_t& lo) {
+  constexpr float L = Widen<T>::kBf16 ? 0x1p60f : 0x1p5f;
+  hi = Widen<T>::pack(x, y);
+  const float2 h = unpack<T>(hi);
+  lo = Widen<T>::pack(fmaxf(x - h.x, -L), fmaxf(y - h.y, -L));
+}
+
 // The distinct ids >= 0 of ids[0..n), n <= 256, in the order they first occur, by threads 0..255.
 // `runs` is scratch of 256; the list and its length end in `list` and *count.  Every thread of the CTA calls it.
 __device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, int32_t* list, uint32_t* count,

@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     float unit = 1.0f;
     if (wide && !Widen<T>::kBf16) {
       float m = 0;
-      for (uint64_t i = threadIdx.x - 64; i < a.n_scale; i += 128 * G) {
+#pragma unroll 8
+      for (uint32_t i = threadIdx.x - 64; i < (uint32_t)a.n_scale; i += 128 * G) {
         const float s = fabsf(a.scale[i]);
         if (s <= 3e38f) m = fmaxf(m, s);
       }
@@ -359,10 +360,10 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       }
       // A group skips the stage's uses by the others, and a barrier tells its phases apart by their parity alone: the
       // stage's last products have ended (which no phase can overtake, as this step is still to come), then its
-      // load is the one waited for.
-      ok = (P == 1 || wait_free(s, turn)) && mbar_wait_warp(full + 8 * s, turn, failed);
+      // load is the one waited for.  In wide steps the group waited for those products before its last step's stores.
+      ok = (P == 1 || wide || wait_free(s, turn)) && mbar_wait_warp(full + 8 * s, turn, failed);
       // P = 2: the stage was loaded after its last products ended, and with them the slot's
-      if (P == 1) ok = ok && mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed);
+      if (P == 1 && !wide) ok = ok && mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed);
       if (!ok) break;
       fence_after();
       if (!BACK) {
@@ -383,27 +384,46 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         }
         tmem_st32(widened(slot) + lanes, v);
       } else {
+        const uint32_t from = at + k * 64 * 128 + row;
+        if (!wide) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint32_t from = at + (k * 64 + half * 32) * 128 + row;
-          uint32_t b[32], w[16], rest[16];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t b[32], w[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + j * 128));
-          if (!wide) {
+            for (int j = 0; j < 32; ++j)
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b[j]) : "r"(from + (half * 32 + j) * 128));
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = widen2<T>(b[2 * j + 1] * 256u + b[2 * j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w4 : 0][32 * half + 2 * j]);
-              const float2 y = widen2_float(b[2 * j + 1] * 256u + b[2 * j]),
-                           z = widen2_float(b[2 * j + 3] * 256u + b[2 * j + 2]);
-              split_pair<T>(y.x * x.x, y.y * x.y, w[j], rest[j]);
-              split_pair<T>(z.x * x.z, z.y * x.w, w[j + 1], rest[j + 1]);
-            }
-            tmem_st16(widened(slot) + 32 + half * 16 + lanes, rest);
+            tmem_st16(widened(slot) + half * 16 + lanes, w);
           }
-          tmem_st16(widened(slot) + half * 16 + lanes, w);
+        } else {
+          // all of the thread's bytes, four to a word, and half of the products before the slot is waited for
+          uint32_t b[16], w[16], rest[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            uint32_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x[i]) : "r"(from + (4 * j + i) * 128));
+            b[j] = __byte_perm(x[1] * 256u + x[0], x[3] * 256u + x[2], 0x5410);
+          }
+          auto scaled = [&](int half) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 x = *reinterpret_cast<const float4*>(&scale_s[BACK ? w4 : 0][32 * half + 4 * j]);
+              const float2 y = widen2_float(b[8 * half + j]), z = widen2_float(b[8 * half + j] >> 16);
+              split_scaled<T>(y.x * x.x, y.y * x.y, w[2 * j], rest[2 * j]);
+              split_scaled<T>(z.x * x.z, z.y * x.w, w[2 * j + 1], rest[2 * j + 1]);
+            }
+          };
+          scaled(0);
+          ok = P == 1 ? mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed) : wait_free(s, turn);
+          if (!ok) break;
+          fence_after();
+          tmem_st16(widened(slot) + lanes, w);
+          tmem_st16(widened(slot) + 32 + lanes, rest);
+          scaled(1);
+          tmem_st16(widened(slot) + 16 + lanes, w);
+          tmem_st16(widened(slot) + 48 + lanes, rest);
         }
       }
       announce(slot);
