@@ -12,7 +12,8 @@
 #include "ecf8.h"
 #include "ecf8_tc.cuh"
 
-namespace ecf8_linear_impl {
+// hidden: two copies of the library in one process (the bounds-checked one beside the other) share nothing
+namespace ecf8_linear_impl __attribute__((visibility("hidden"))) {
 
 using namespace ecf8_tc;
 

@@ -44,7 +44,7 @@
 
 #include "ecf8_linear.cuh"
 
-namespace ecf8_linear_impl {
+namespace ecf8_linear_impl __attribute__((visibility("hidden"))) {
 
 // sum over r of p[t][r] f[a][c][r] (or f[a][r][c]): the adapter's part of one output.
 template <class T>

@@ -1,5 +1,7 @@
 """Linear layers on the GPU in the forms that large and unusual calls take,
 against the formula in 64 bits."""
+import ctypes
+
 import pytest
 
 from test_gpu_linear import Case, env  # noqa: F401
@@ -55,3 +57,43 @@ def test_requests_that_overlap_leave_the_other_rows(env, rows, n, k, rank):
     keep[8:40] = False
     c.near(y[keep], want[keep], size[keep], k + rank, pairs[keep])
     c.near(grads[0][keep], wdx[keep], sizex[keep], n + rank, pairsx[keep])
+
+
+class Checked:
+    """Forward and backward of a case through the bounds-checked build, beside the library itself."""
+
+    def __init__(self, c):
+        L, torch = c.env
+        from lossless_fp8_weight_b200 import _build
+        self.c, self.so = c, ctypes.CDLL(_build.build(checked=True))
+        self.so.ecf8_linear_forward.argtypes = L._lib.ecf8_linear_forward.argtypes
+        self.so.ecf8_linear_backward.argtypes = L._lib.ecf8_linear_backward.argtypes
+
+    def run(self):
+        """[y, u, dx, da, db] and the status."""
+        c, torch = self.c, self.c.env[1]
+        y = torch.zeros(c.rows, c.n, dtype=c.dtype, device="cuda")
+        u = torch.zeros(c.rows, c.rank, device="cuda")
+        grads = [torch.zeros_like(t) for t in (c.x, c.a, c.b)]
+        q, s = c.linear._requests(c.requests), torch.cuda.current_stream().cuda_stream
+        rest = (c.ws.data_ptr(), c.ws.numel(), c.status.data_ptr(), s)
+        assert self.so.ecf8_linear_forward(c.linear._ref, q, c.x.data_ptr(), c.k, y.data_ptr(), c.n, c.rows,
+                                           u.data_ptr(), *rest) == 0
+        assert self.so.ecf8_linear_backward(c.linear._ref, q, c.x.data_ptr(), c.k, c.dy.data_ptr(), c.n, u.data_ptr(),
+                                            grads[0].data_ptr(), c.k, grads[1].data_ptr(), grads[2].data_ptr(), c.rows,
+                                            *rest) == 0
+        torch.cuda.synchronize()
+        status = int(c.status.item())
+        c.status.zero_()
+        return [y, u, *grads], status
+
+
+@pytest.mark.parametrize("rows,n,k", [(40, 256, 4096), (600, 3328, 512)])
+def test_two_copies_of_the_library_in_one_process(env, rows, n, k):
+    """The checked build beside the other one: the same bits, whichever ran first."""
+    L, torch = env
+    c = Case(env, rows, n, k, 16, 2, [rows - 9], [1], "bf16", "row", seed=32)
+    y, u = c.forward()
+    want = [y, u, *c.backward(u)]
+    got, status = Checked(c).run()
+    assert status == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
