@@ -166,6 +166,7 @@ struct ShrinkArgs {
   int32_t* row_id;       // written: the adapter of every row, -1 for none
   float* p;              // rows x rank
   int32_t* status;
+  Limits limits;
 };
 
 constexpr int kShrinkThreads = 320;
@@ -175,16 +176,17 @@ __global__ void __launch_bounds__(kShrinkThreads)
     shrink_tc(const __grid_constant__ CUtensorMap map_f, const __grid_constant__ CUtensorMap map_q,
               const __grid_constant__ ShrinkArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed_s;
   __shared__ int32_t ids[256], runs[256], list[256];
   __shared__ uint32_t count_s, warp_sum[8];
-  volatile int* failed = &failed_s;
+  const Waits waits{&failed_s, a.limits.cycles};
 
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t f_bytes = 16384, q_bytes = a.bt * 128, stage_bytes = f_bytes + q_bytes;
-  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, done = empty + 8 * kMaxStages;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, done = empty + 8 * kMaxStages,
+                 spent = done + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
   const uint32_t chunk = blockIdx.x / a.split;
@@ -202,10 +204,11 @@ __global__ void __launch_bounds__(kShrinkThreads)
   if (threadIdx.x < 256) ids[threadIdx.x] = -1;
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, i == 0 ? 1 + a.limits.missing : 1);
       mbar_init(empty + 8 * i, 1);
     }
     mbar_init(done, 1);
+    mbar_init(spent, 1);
     failed_s = 0;
     mbar_init_fence();
   }
@@ -262,13 +265,11 @@ __global__ void __launch_bounds__(kShrinkThreads)
   }
   const uint32_t mine = count_s - first < a.per ? count_s - first : a.per;
 
+  uint32_t next = 0, next_turn = 0;  // warp 0: the next stage to load, and the parity of its use
   if (warp == 0) {
-    uint32_t s = 0, turn = 0;  // stage, and the parity of its use
-    bool ok = true;
     for (uint32_t i = 0; i < nb; ++i) {
-      ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
-      if (!ok) break;
-      const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
+      if (!mbar_wait_lanes(empty + 8 * next, next_turn ^ 1, waits)) break;
+      const uint32_t at = base + next * stage_bytes, bar = full + 8 * next;
       const int32_t j = (int32_t)((b0 + i) * 64);
       if (elect_one()) {
         mbar_expect(bar, q_bytes + mine * a.rank * 128);
@@ -279,15 +280,14 @@ __global__ void __launch_bounds__(kShrinkThreads)
       for (uint32_t k = lane; k < mine; k += 32)
         tma_load(at + k * pad * 128, &map_f, j, list[first + k] * (int32_t)a.rank, bar);
       __syncwarp();
-      if (++s == a.stages) s = 0, turn ^= 1;
+      if (++next == a.stages) next = 0, next_turn ^= 1;
     }
-    if (!ok) drain(full, s, turn, a.stages);
   } else if (warp == 1) {
     const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128, a.bt);
     bool ok = true;
     uint32_t s = 0, turn = 0;
     for (uint32_t i = 0; i < nb; ++i) {
-      ok = mbar_wait(full + 8 * s, turn, failed);
+      ok = mbar_wait_lanes(full + 8 * s, turn, waits);
       if (!ok) break;
       fence_after();
       const uint64_t f = desc_k128(base + s * stage_bytes), q = desc_k128(base + s * stage_bytes + f_bytes);
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
     const int quarter = warp % 4, half = (warp - 2) / 4;
     const uint32_t row = quarter * 32 + lane;
     const uint32_t slot = row / pad, r = row % pad;
-    const bool ok = mbar_wait_warp(done, 0, failed);
+    const bool ok = mbar_wait(done, 0, waits);
     if (ok && quarter * 32 < mine * pad) {
       fence_after();
       const int32_t id = slot < mine && r < a.rank ? list[first + slot] : -2;
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
   if (a.split > 1) {
     __syncwarp();
     cluster_sync();
-    if (warp >= 2 && !*failed) {
+    if (warp >= 2 && !failed_s) {
       // a thread four ranks at a time (of one adapter: pad is a multiple of 8)
       const uint32_t wide = mine * pad / 4, lo = a.bt * crank / a.split, hi = a.bt * (crank + 1) / a.split;
       for (uint32_t i = threadIdx.x - 64; i < (hi - lo) * wide; i += 256) {
@@ -344,8 +344,12 @@ __global__ void __launch_bounds__(kShrinkThreads)
   fence_before();
   __syncthreads();
   fence_after();
+  if (failed_s) {
+    if (warp == 0) drain_loads(full, next, next_turn, a.stages, waits);
+    if (warp == 1) drain_products<1>(spent, 0, waits);
+  }
   if (warp == 1) tmem_free<1>(tmem, columns);
-  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+  if (threadIdx.x == 0 && failed_s && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
 // Rows of bytes copied to rows whose bases and distances TMA takes (multiples of 16 bytes), for operands that are
@@ -429,6 +433,7 @@ struct OuterArgs {
   const float* alpha;
   OuterSide side[2];
   int32_t* status;
+  Limits limits;
 };
 
 constexpr int kOuterThreads = 320;
@@ -450,18 +455,18 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
              const __grid_constant__ CUtensorMap map_q1, const __grid_constant__ CUtensorMap map_p1,
              const __grid_constant__ OuterArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 1];
+  __shared__ __align__(8) uint64_t bars[3 * kMaxStages + 2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed_s;
   __shared__ int32_t begin_s[kWindow], end_s[kWindow];
   __shared__ uint32_t warp_sum[kOuterThreads / 32];
-  volatile int* failed = &failed_s;
+  const Waits waits{&failed_s, a.limits.cycles};
 
   const uint32_t pad = padded(a.rank), n = part_columns(a.rank);
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t q_bytes = 16384, stage_bytes = q_bytes + n * 128;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
-                 done = ready + 8 * kMaxStages;
+                 done = ready + 8 * kMaxStages, spent = done + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t crank = a.split > 1 ? cluster_rank() : 0;
   const uint32_t tile = blockIdx.x / a.split, which = tile < a.side[0].tiles ? 0 : 1;
@@ -478,11 +483,12 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
   }
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, i == 0 ? 1 + a.limits.missing : 1);
       mbar_init(empty + 8 * i, 1);
       mbar_init(ready + 8 * i, 8);
     }
     mbar_init(done, 1);
+    mbar_init(spent, 1);
     failed_s = 0;
     mbar_init_fence();
   }
@@ -529,7 +535,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
         const uint32_t valid = (uint32_t)min((int64_t)64, (int64_t)end_s[k] - t0);
         const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
         if (warp == 0) {
-          ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+          ok = mbar_wait_lanes(empty + 8 * s, turn ^ 1, waits);
           if (!ok) break;
           if (elect_one()) {
             mbar_expect(bar, stage_bytes);
@@ -539,7 +545,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
           }
           __syncwarp();
         } else if (warp == 1) {
-          ok = mbar_wait(ready + 8 * s, turn, failed);
+          ok = mbar_wait_lanes(ready + 8 * s, turn, waits);
           if (!ok) break;
           fence_after();
           const uint64_t q = desc_mn128(at, 8192), p = desc_mn128(at + q_bytes, 8192);
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
           }
           __syncwarp();
         } else {
-          ok = mbar_wait_warp(bar, turn, failed);
+          ok = mbar_wait(bar, turn, waits);
           if (!ok) break;
           if (valid < 64) {
             // whole 128-byte rows, so the swizzle does not matter; boxes of 64 rows follow each other
@@ -572,7 +578,6 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     __syncwarp();
     __syncthreads();
   }
-  if (warp == 0 && !ok) drain(full, s, turn, a.stages);
   if (warp == 1 && used) {
     if (ok && elect_one()) mma_commit<1>(done, 0);
     __syncwarp();
@@ -584,7 +589,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     const uint32_t row = quarter * 32 + lane;
     const uint64_t c = c0 + row;
     if (used) {
-      ok = ok && mbar_wait_warp(done, 0, failed);
+      ok = ok && mbar_wait(done, 0, waits);
       if (ok) fence_after();
     }
     if (ok)
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
   if (a.split > 1) {
     __syncwarp();
     cluster_sync();
-    if (warp >= 2 && !*failed) {
+    if (warp >= 2 && !failed_s) {
       const uint32_t k = threadIdx.x - 64, row = k % 32 * 4;
       const uint64_t c = c0 + row;
       const uint32_t lo = a.rank * crank / a.split, hi = a.rank * (crank + 1) / a.split;
@@ -635,8 +640,12 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
   fence_before();
   __syncthreads();
   fence_after();
+  if (failed_s) {
+    if (warp == 0) drain_loads(full, s, turn, a.stages, waits);
+    if (warp == 1) drain_products<1>(spent, 0, waits);
+  }
   if (warp == 1) tmem_free<1>(tmem, columns);
-  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+  if (threadIdx.x == 0 && failed_s && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
 // v (blockIdx.y = 0) and u (1), either of which may be absent: what is read, and what is written of it.
@@ -718,6 +727,13 @@ __global__ void __launch_bounds__(128) outer_simple(const float* p, uint32_t ran
     for (uint32_t r = 0; r < 8; ++r)
       if (r < nr) put(out + (uint64_t)a * f_adapter + (r0 + r) * sr + c * sc, alpha[a] * acc[r]);
 }
+
+#ifdef ECF8_CHECKED
+Limits g_limits[3];  // of the projection, the adapters' first product, their gradients
+Limits limits_of(int kernel) { return g_limits[kernel]; }
+#else
+Limits limits_of(int) { return Limits{}; }
+#endif
 
 constexpr uint64_t kGridY = 65535;
 constexpr uint64_t kMost = 1ull << 31;  // rows, columns and adapters stay below it
@@ -935,6 +951,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.out_stride = out_stride;
   a.out_vector = aligned(out, 8) && out_stride % 4 == 0 && cols % 4 == 0;
   a.status = d_status;
+  a.limits = limits_of(0);
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mw, mq;
@@ -987,6 +1004,7 @@ int shrink_tensor(const T* q, uint64_t q_stride, uint64_t rows, const T* f, uint
   a.row_id = row_id;
   a.p = p;
   a.status = d_status;
+  a.limits = limits_of(1);
   const CUtensorMapDataType type =
       Widen<T>::kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   CUtensorMap mf, mq;
@@ -1035,6 +1053,7 @@ int outer_tensor(const Outer* sides, int n_sides, uint32_t rank, uint32_t n_adap
   a.count = req->count;
   a.alpha = alpha;
   a.status = d_status;
+  a.limits = limits_of(2);
   PartsArgs b{};
   b.rows = rows;
   b.rank = rank;
@@ -1198,6 +1217,14 @@ int backward(const ecf8_linear* l, const ecf8_requests* q, const void* x, uint64
 }  // namespace
 
 extern "C" {
+
+#ifdef ECF8_CHECKED
+// For tests, in this build only: the limit of the waits of one kind of kernel (0 the projection, 1 the adapters' first
+// product, 2 their gradients), and arrivals that the first load's barrier waits for in vain.
+void ecf8_checked_limits(int kernel, long long cycles, uint32_t missing) {
+  g_limits[kernel] = cycles ? Limits{cycles, missing} : Limits{};
+}
+#endif
 
 size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows) {
   return lin && rows < kMost ? plan_of(lin, rows).total : 0;

@@ -123,16 +123,25 @@ __device__ inline void distinct(const int32_t* ids, uint32_t n, int32_t* runs, i
   __syncthreads();
 }
 
-// A CTA does not end while its loads are in flight.  The next use of a stage would have been `s` with parity `turn`:
-// waits, with a limit, for the last use of every stage (at once where it has ended, or where there was none).
-__device__ inline void drain(uint32_t full, uint32_t s, uint32_t turn, uint32_t stages) {
-  for (uint32_t i = 0; i < stages; ++i) {
-    const uint32_t last = i < s ? turn : turn ^ 1;
-    const long long start = clock64();
-    while (!mbar_try(full + 8 * i, last) && clock64() - start < kWaitCycles) {
-    }
-  }
+// A CTA that has failed does not end before the loads and products that it started.  One warp each: the loads, where
+// the next use of a stage would have been `s` with parity `turn` (a wait for the last use of every stage; at once where
+// there was none), and the products, whose end arrives on `spent` of the CTA that issued them.
+__device__ inline void drain_loads(uint32_t full, uint32_t s, uint32_t turn, uint32_t stages, const Waits& w) {
+  for (uint32_t i = 0; i < stages; ++i) mbar_wait_out(full + 8 * i, i < s ? turn : turn ^ 1, w);
 }
+template <int P>
+__device__ inline void drain_products(uint32_t spent, uint32_t rank, const Waits& w) {
+  if (elect_one()) mma_commit<P>(spent, 1u << rank);
+  __syncwarp();
+  mbar_wait_out(spent, 0, w);
+}
+
+// How a launch waits.  The bounds-checked build can set it: a short limit, and one arrival more than will come on the
+// first load's barrier.
+struct Limits {
+  long long cycles = kWaitCycles;
+  uint32_t missing = 0;
+};
 
 struct ProductArgs {
   uint64_t rows, cols, len;
@@ -153,6 +162,7 @@ struct ProductArgs {
   uint64_t out_stride;
   uint32_t out_vector;   // 4 columns of an output row are one aligned 8-byte store
   int32_t* status;
+  Limits limits;
 };
 
 constexpr uint32_t kMaxStages = 16, kSlots = 8;

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   const uint32_t slot_bits = (P == 2 ? 3 : 2) - (wide ? 1 : 0), slot_mask = (1u << slot_bits) - 1;
   const uint32_t slot_columns = wide ? 64 : 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2 * kSlots + 2];
   __shared__ uint32_t tmem_base;
   __shared__ int failed_s;
   __shared__ float unit_s;
@@ -156,13 +156,13 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   __shared__ __align__(16) float scale_s[BACK ? 4 * G : 1][64];
   __shared__ int32_t ids[256], runs[256], list[256];
   __shared__ uint32_t count_s, warp_sum[8], apart_s;
-  volatile int* failed = &failed_s;
+  const Waits waits{&failed_s, a.limits.cycles};
 
   const uint32_t base = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t rows_here = a.bt / P;  // rows of q that this CTA loads
   const uint32_t w_bytes = 8192 * KB, q_bytes = rows_here * 128 * KB, stage_bytes = w_bytes + q_bytes;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
-                 freed = ready + 8 * kSlots, done = freed + 8 * kSlots;
+                 freed = ready + 8 * kSlots, done = freed + 8 * kSlots, spent = done + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t cluster = P * a.split, crank = cluster > 1 ? cluster_rank() : 0;
   const uint32_t side = crank % P, part = crank / P, leader = part * P;
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
 
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < a.stages; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, i == 0 ? 1 + a.limits.missing : 1);
       mbar_init(empty + 8 * i, 1);
     }
     for (uint32_t i = 0; i < most_slots; ++i) {
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       mbar_init(freed + 8 * i, 1);
     }
     mbar_init(done, 1);
+    mbar_init(spent, 1);
     failed_s = 0;
     apart_s = 0;
     unit_s = 1.0f;
@@ -217,19 +218,19 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     adapter_steps = all / a.split + (part < all % a.split ? 1 : 0);
   };
 
+  uint32_t next = 0, next_turn = 0;  // warp 0: the next stage to load, and the parity of its use
   if (warp == 0) {
     if (elect_one()) {
       tma_prefetch(&map_w);
       tma_prefetch(&map_q);
     }
-    uint32_t s = 0, turn = 0;  // stage, and the parity of its use
     bool ok = true;
     for (uint32_t i = 0; i < nb; ++i) {
       // a stage is free when its products have ended, and so have the warps that widened for them
       // (a wait for the phase before the first passes at once)
-      ok = mbar_wait(empty + 8 * s, turn ^ 1, failed);
+      ok = mbar_wait_lanes(empty + 8 * next, next_turn ^ 1, waits);
       if (!ok) break;
-      const uint32_t at = base + s * stage_bytes, bar = full + 8 * s;
+      const uint32_t at = base + next * stage_bytes, bar = full + 8 * next;
       const int32_t j = (int32_t)((b0 + i) * 64 * KB);
       if (elect_one()) {
         mbar_expect(bar, stage_bytes);
@@ -240,9 +241,8 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           tma_load(at + w_bytes + k * rows_here * 128, &map_q, j + 64 * k, (int32_t)(t0 + side * rows_here), bar);
       }
       __syncwarp();
-      if (++s == a.stages) s = 0, turn ^= 1;
+      if (++next == a.stages) next = 0, next_turn ^= 1;
     }
-    if (!ok) drain(full, s, turn, a.stages);
     find_adapters();
   } else if (warp == 1) {
     if (side != 0) {
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         for (int k = 0; k < KB && ok; ++k, ++g) {
           // the warps that report a step ready have waited for their CTA's tiles
           const uint32_t slot = P == 2 ? s : g & slot_mask;
-          ok = mbar_wait<P == 2>(ready + 8 * slot, P == 2 ? turn : g >> slot_bits & 1, failed);
+          ok = mbar_wait_lanes<P == 2>(ready + 8 * slot, P == 2 ? turn : g >> slot_bits & 1, waits);
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes + k * rows_here * 128);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (P == 2) {
         const uint32_t idesc_pair = idesc_f16(true, 128 * P, a.bt);
         for (uint32_t i = 0; i < adapter_steps && ok; ++i, ++g) {
-          ok = mbar_wait<true>(ready + 8 * s, turn, failed);
+          ok = mbar_wait_lanes<true>(ready + 8 * s, turn, waits);
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes);
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     // of the group's last step, which lie in them and are later ones.
     static_assert(P == 1 || (kSlots == 8 && G == 4), "a group's last step is four stages back in a ring of eight");
     auto wait_free = [&](uint32_t s, uint32_t turn) {
-      return wide ? mbar_wait_warp(empty + 8 * (s ^ 4), s >= 4 ? turn : turn ^ 1, failed)
-                  : mbar_wait_warp(empty + 8 * s, turn ^ 1, failed);
+      return wide ? mbar_wait(empty + 8 * (s ^ 4), s >= 4 ? turn : turn ^ 1, waits)
+                  : mbar_wait(empty + 8 * s, turn ^ 1, waits);
     };
     bool ok = true;
     uint32_t g = group, s = group / KB, turn = 0;
@@ -361,9 +361,9 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       // A group skips the stage's uses by the others, and a barrier tells its phases apart by their parity alone: the
       // stage's last products have ended (which no phase can overtake, as this step is still to come), then its
       // load is the one waited for.  In wide steps the group waited for those products before its last step's stores.
-      ok = (P == 1 || wide || wait_free(s, turn)) && mbar_wait_warp(full + 8 * s, turn, failed);
+      ok = (P == 1 || wide || wait_free(s, turn)) && mbar_wait(full + 8 * s, turn, waits);
       // P = 2: the stage was loaded after its last products ended, and with them the slot's
-      if (P == 1 && !wide) ok = ok && mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed);
+      if (P == 1 && !wide) ok = ok && mbar_wait(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, waits);
       if (!ok) break;
       fence_after();
       if (!BACK) {
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
             }
           };
           scaled(0);
-          ok = P == 1 ? mbar_wait_warp(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, failed) : wait_free(s, turn);
+          ok = P == 1 ? mbar_wait(freed + 8 * slot, (g >> slot_bits & 1) ^ 1, waits) : wait_free(s, turn);
           if (!ok) break;
           fence_after();
           tmem_st16(widened(slot) + lanes, w);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
         if (s >= a.stages) s -= a.stages, turn ^= 1;
       }
     }
-    ok = ok && mbar_wait_warp(done, 0, failed);
+    ok = ok && mbar_wait(done, 0, waits);
     if (ok) fence_after();
     wait_predecessor();  // row_id and p are there, and nothing before this call reads the output any more
     if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");  // apart_s
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     __syncwarp();
     cluster_sync();
     // each CTA adds up and writes its share of the tile's rows, a thread four columns at a time
-    if (warp >= 2 && !*failed) {
+    if (warp >= 2 && !failed_s) {
       const uint32_t n = threadIdx.x - 64, row = n % 32 * 4;
       const uint64_t c = c0 + row;
       const uint32_t lo = a.bt * part / a.split, hi = a.bt * (part + 1) / a.split;
@@ -570,6 +570,11 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       }
     }
   }
+  __syncthreads();  // no wait of this CTA can fail any more
+  if (failed_s) {
+    if (warp == 0) drain_loads(full, next, next_turn, a.stages, waits);
+    if (warp == 1 && side == 0) drain_products<P>(spent, crank, waits);
+  }
   if (cluster > 1) {
     __syncwarp();
     cluster_sync();  // no CTA leaves while another reads its memory or arrives on its barriers
@@ -578,7 +583,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   __syncthreads();
   fence_after();
   if (warp == 1) tmem_free<P>(tmem, columns);
-  if (threadIdx.x == 0 && *failed && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
+  if (threadIdx.x == 0 && failed_s && a.status) atomicOr(a.status, ECF8_STATUS_TIMEOUT);
 }
 
 template <class T, int P, int KB, int G, int BACK>

@@ -1,7 +1,10 @@
 // Thin wrappers of the sm_100a instructions the tensor-core kernels use:
 // mbarriers, TMA tile loads, tcgen05 (tensor memory, matrix products).
-// Every wait has a limit in clock cycles, after which it fails, marks the CTA
-// as failed and lets every other wait of the CTA fail as well.
+// Every wait for an mbarrier has a limit in clock cycles, after which it fails,
+// marks the CTA as failed and lets every other such wait of the CTA fail as well.
+// The others end by construction: every thread arrives at the barriers of the
+// CTA and the cluster whether it has failed or not, a kernel that is waited for
+// has what it needs to end, and tensor memory is freed by CTAs that do.
 #ifndef ECF8_TC_CUH_
 #define ECF8_TC_CUH_
 
@@ -13,6 +16,11 @@
 namespace ecf8_tc {
 
 constexpr long long kWaitCycles = 4000000000ll;  // about two seconds
+
+struct Waits {
+  volatile int* failed;  // in shared memory
+  long long limit;       // clock cycles of a wait
+};
 
 __device__ inline uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -53,30 +61,48 @@ __device__ inline bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
   return ok != 0;
 }
-// Waits for the phase of this parity to complete; false when the limit ran out
-// or another wait of the CTA has failed.  The clock is read rarely: waiting
-// warps should leave the issue slots to the working ones.
+// Waits for the phase of this parity to complete; false when the limit ran out or another wait of the CTA has failed.
+// The clock is read rarely: waiting warps should leave the issue slots to the working ones.
 template <bool CLUSTER = false>
-__device__ inline bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* failed) {
+__device__ inline bool mbar_poll(uint32_t bar, uint32_t parity, const Waits& w) {
   if (mbar_try<CLUSTER>(bar, parity)) return true;
   const long long start = clock64();
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (mbar_try<CLUSTER>(bar, parity)) return true;
-    if (*failed) return false;
-    if (clock64() - start > kWaitCycles) {
-      *failed = 1;
+    if (*w.failed) return false;
+    if (clock64() - start > w.limit) {
+      *w.failed = 1;
       return false;
     }
   }
 }
-
-// mbar_wait of a whole warp through one lane: 32 lanes that poll take turns (some 500 clocks a wait, measured).
-__device__ inline bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile int* failed) {
+// The same for a whole warp, with one answer for all lanes: each has a limit of its own, and a warp that parted could not
+// elect a lane any more.  Every lane polls, which suits a warp that loads or issues products (with one lane polling 8192
+// rows of 14336x4096 took 1010 us, 890 so).
+template <bool CLUSTER = false>
+__device__ inline bool mbar_wait_lanes(uint32_t bar, uint32_t parity, const Waits& w) {
+  const bool ok = __all_sync(~0u, mbar_poll<CLUSTER>(bar, parity, w));
+  __syncwarp();
+  return ok;
+}
+// One lane polls: in a warp that widens, 32 take turns (some 500 clocks a wait, measured).
+__device__ inline bool mbar_wait(uint32_t bar, uint32_t parity, const Waits& w) {
   bool ok = true;
-  if (threadIdx.x % 32 == 0) ok = mbar_wait(bar, parity, failed);
-  return __all_sync(~0u, ok);
+  if (threadIdx.x % 32 == 0) ok = mbar_poll(bar, parity, w);
+  ok = __all_sync(~0u, ok);
+  __syncwarp();  // what the lane that waited may read, all may
+  return ok;
+}
+// The same for what has to end before a CTA that has failed does.
+__device__ inline void mbar_wait_out(uint32_t bar, uint32_t parity, const Waits& w) {
+  if (threadIdx.x % 32 == 0) {
+    const long long start = clock64();
+    while (!mbar_try(bar, parity) && clock64() - start < w.limit) {
+    }
+  }
+  __syncwarp();
 }
 
 // True in one lane of a converged warp.  Around it the warp stays together, so that addresses and descriptors are

@@ -97,3 +97,24 @@ def test_two_copies_of_the_library_in_one_process(env, rows, n, k):
     want = [y, u, *c.backward(u)]
     got, status = Checked(c).run()
     assert status == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2], ids=["projection", "first product", "gradients"])
+@pytest.mark.parametrize("rows,n,k", [(40, 256, 4096), (600, 3328, 512)])
+def test_a_wait_that_runs_out_is_reported(env, rows, n, k, kernel):
+    """A barrier that waits for an arrival too many, with a limit of a millisecond: the calls end, say so, and leave the
+    device as it was.  The bounds-checked build alone can be told to."""
+    L, torch = env
+    c = Case(env, rows, n, k, 16, 2, [rows - 9], [1], "bf16", "row", seed=32)
+    checked = Checked(c)
+    want, status = checked.run()
+    assert status == 0
+    limits = checked.so.ecf8_checked_limits
+    limits.argtypes = [ctypes.c_int, ctypes.c_longlong, ctypes.c_uint32]
+    limits(kernel, 2_000_000, 1)
+    try:
+        assert checked.run()[1] == L.STATUS_TIMEOUT
+    finally:
+        limits(kernel, 0, 0)
+    got, status = checked.run()
+    assert status == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
