@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kShrinkThreads)
       for (uint32_t i = threadIdx.x - 64; i < (hi - lo) * wide; i += 256) {
         const uint32_t t = lo + i / wide, row = i % wide * 4, slot = row / pad, r = row % pad;
         if (ids[t] != list[first + slot]) continue;
-        const float4 d = cluster_sum4(base + (t * 128 + row) * 4, 0, 1, a.split);
+        const float4 d = cluster_sum4(base + (t * 128 + row) * 4, a.split);
         float* p = a.p + (t0 + t) * a.rank + r;
         if (r < a.rank) p[0] = d.x;
         if (r + 1 < a.rank) p[1] = d.y;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
       const uint64_t c = c0 + row;
       const uint32_t lo = a.rank * crank / a.split, hi = a.rank * (crank + 1) / a.split;
       for (uint32_t r = lo + k / 32; r < hi; r += 8) {
-        const float4 d = cluster_sum4(base + (r * 128 + row) * 4, 0, 1, a.split);
+        const float4 d = cluster_sum4(base + (r * 128 + row) * 4, a.split);
         const float y[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -923,11 +923,10 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.blocks = (uint32_t)((len + 64 * kb - 1) / (64 * kb));
   const uint64_t tiles = (cols + 128 * width - 1) / (128 * width), row_tiles = (rows + a.bt - 1) / a.bt;
   if (row_tiles > kGridY) return ECF8_ERR_UNSUPPORTED;
-  // Enough CTAs to keep every SM loading, while each still has a few steps to pipeline.
-  const uint64_t room_for = pair ? 74 : 296;
-  const uint32_t most = 8 / width;
+  // Enough CTAs to keep every SM loading, while each still has a few steps to pipeline.  (Pairs are taken where they need
+  // no split.)
   a.split = 1;
-  while (a.split < most && tiles * row_tiles * a.split * 2 <= room_for && a.blocks / (a.split * 2) >= 2) a.split *= 2;
+  while (!pair && a.split < 8 && tiles * row_tiles * a.split * 2 <= 296 && a.blocks / (a.split * 2) >= 2) a.split *= 2;
   const uint32_t here = a.bt / width, stage = 8192 * kb + here * 128 * kb;
   const uint32_t room = (pair ? 216 * 1024 : 106 * 1024) - 1024;
   const uint32_t fit = room / stage, at_most = pair ? kSlots : kMaxStages;

@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
   const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages, ready = empty + 8 * kMaxStages,
                  freed = ready + 8 * kSlots, done = freed + 8 * kSlots, spent = done + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t cluster = P * a.split, crank = cluster > 1 ? cluster_rank() : 0;
-  const uint32_t side = crank % P, part = crank / P, leader = part * P;
+  // a cluster is a pair, or the parts of a split reduction
+  const uint32_t split = P == 2 ? 1 : a.split, cluster = P * split, crank = cluster > 1 ? cluster_rank() : 0;
+  const uint32_t side = P == 2 ? crank : 0, part = P == 2 ? 0 : crank;
   const uint64_t c0 = ((uint64_t)(blockIdx.x / cluster) * P + side) * 128, t0 = (uint64_t)blockIdx.y * a.bt;
-  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * part / a.split),
-                 b1 = (uint32_t)((uint64_t)a.blocks * (part + 1) / a.split), nb = b1 - b0;
+  const uint32_t b0 = (uint32_t)((uint64_t)a.blocks * part / split),
+                 b1 = (uint32_t)((uint64_t)a.blocks * (part + 1) / split), nb = b1 - b0;
   const uint32_t steps = nb * KB;
 
   if (threadIdx.x == 0) {
@@ -214,8 +215,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     __syncthreads();
     distinct(ids, a.bt, runs, list, &count_s, warp_sum);
     units = count_s * ((a.rank + 15) / 16);
-    const uint32_t all = (units + 1) / 2;  // steps of two units, dealt out to the parts
-    adapter_steps = all / a.split + (part < all % a.split ? 1 : 0);
+    adapter_steps = (units + 1) / 2;
   };
 
   uint32_t next = 0, next_turn = 0;  // warp 0: the next stage to load, and the parity of its use
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     if (side != 0) {
       find_adapters();
     } else {
-      const uint32_t mask = 3u << leader;
+      const uint32_t mask = 3;
       const uint32_t idesc = idesc_f16(Widen<T>::kBf16, 128 * P, a.bt);
       uint32_t g = 0, s = 0, turn = 0;  // 64-wide steps, stage, parity
       bool ok = true;
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
           if (!ok) break;
           fence_after();
           const uint64_t b = desc_k128(base + s * stage_bytes + w_bytes);
-          const uint32_t first = (i * a.split + part) * 2;
+          const uint32_t first = i * 2;
           if (elect_one()) {
             for (uint32_t u = 0; u < 2 && first + u < units; ++u) {
               const uint32_t hi = widened(s) + u * 16;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       fence_before();
       __syncwarp();
       if (lane == 0) {
-        if (P == 2 && side) mbar_arrive_at(ready + 8 * slot, leader);
+        if (P == 2 && side) mbar_arrive_at(ready + 8 * slot, 0);
         else mbar_arrive(ready + 8 * slot);
       }
     };
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       // writes its rows' side of both where the stage's rows were.  What they read is fetched before the wait.
       const uint32_t chunks = (a.rank + 15) / 16;
       for (; g < steps + adapter_steps && ok; g += G) {
-        const uint32_t first = ((g - steps) * a.split + part) * 2;
+        const uint32_t first = (g - steps) * 2;
         uint32_t v[32] = {};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
 #pragma unroll
               for (int q = 0; q < 8; ++q) split_pair<__nv_bfloat16>(y[2 * q], y[2 * q + 1], hi[q], lo[q]);
             } else {
-              for (uint32_t r = 0; r < 2; ++r) cluster_stu(smem_addr(&apart_s), leader + r, 1);
+              for (uint32_t r = 0; r < 2; ++r) cluster_stu(smem_addr(&apart_s), r, 1);
             }
           }
           if (!waited) {
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
 
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
     T* out = static_cast<T*>(a.out);
-    if (a.split == 1) {
+    if (split == 1) {
       const bool apart = P == 2 && apart_s;
       if (ok)
         for (uint32_t t = group * 16; t < a.bt; t += 16 * G) {
@@ -527,38 +527,31 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       }
     }
   }
-  if (a.split > 1) {
+  if (split > 1) {
     __syncwarp();
     cluster_sync();
     // each CTA adds up and writes its share of the tile's rows, a thread four columns at a time
     if (warp >= 2 && !failed_s) {
       const uint32_t n = threadIdx.x - 64, row = n % 32 * 4;
       const uint64_t c = c0 + row;
-      const uint32_t lo = a.bt * part / a.split, hi = a.bt * (part + 1) / a.split;
+      const uint32_t lo = a.bt * part / split, hi = a.bt * (part + 1) / split;
       float scale[4];
-      bool divides[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         scale[k] = 1.0f;
         if (c + k < a.cols)
           scale[k] = a.n_scale == 0 ? 1.0f : a.n_scale == 1 ? a.scale[0] : BACK ? 1.0f / unit_s : a.scale[c + k];
-        divides[k] = fabsf(scale[k]) >= 0x1p-40f && fabsf(scale[k]) <= 0x1p40f;
       }
-      bool apart = false;
-      if (P == 2)
-        for (uint32_t r = 0; r < a.split; ++r) apart |= cluster_ldu(cluster_map(smem_addr(&apart_s), r * P + side)) != 0;
       for (uint32_t t = lo + n / 32; t < hi; t += 4 * G) {
         const uint64_t tt = t0 + t;
         if (tt >= a.rows || c >= a.cols) continue;
-        const float4 sum = cluster_sum4(base + (t * 128 + row) * 4, side, P, a.split);
+        const float4 sum = cluster_sum4(base + (t * 128 + row) * 4, split);
         float y[4] = {sum.x * scale[0], sum.y * scale[1], sum.z * scale[2], sum.w * scale[3]};
-        const int32_t id = a.rank && (P == 1 || apart) ? a.row_id[tt] : -1;
+        const int32_t id = a.rank ? a.row_id[tt] : -1;
         if (id >= 0)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (c + k < a.cols)
-              y[k] += P == 1 ? adapter_part<T>(a, id, tt, c + k, 0, a.rank)
-                             : left_out<T>(a, id, tt, c + k, scale[k], divides[k]);
+            if (c + k < a.cols) y[k] += adapter_part<T>(a, id, tt, c + k, 0, a.rank);
         T* out = static_cast<T*>(a.out) + tt * a.out_stride + c;
         if (a.out_vector) {  // the columns are a multiple of 16
           *reinterpret_cast<uint2*>(out) = make_uint2(Widen<T>::pack(y[0], y[1]), Widen<T>::pack(y[2], y[3]));

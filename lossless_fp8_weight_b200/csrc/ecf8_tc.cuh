@@ -269,13 +269,8 @@ __device__ inline uint32_t cluster_map(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
   return a;
 }
-__device__ inline uint32_t cluster_ldu(uint32_t mapped) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapped) : "memory");
-  return v;
-}
-// Adds up to 8 CTAs' four floats at this offset, ranks first, first + step, ..., in that order.
-__device__ inline float4 cluster_sum4(uint32_t addr, uint32_t first, uint32_t step, uint32_t count) {
+// Adds up to 8 CTAs' four floats at this offset, in the order of their ranks.
+__device__ inline float4 cluster_sum4(uint32_t addr, uint32_t count) {
   float4 v[8];
 #pragma unroll
   for (uint32_t r = 0; r < 8; ++r) {
@@ -283,7 +278,7 @@ __device__ inline float4 cluster_sum4(uint32_t addr, uint32_t first, uint32_t st
     if (r < count)
       asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                    : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
-                   : "r"(cluster_map(addr, first + r * step)));
+                   : "r"(cluster_map(addr, r)));
   }
   float4 s = v[0];
 #pragma unroll
