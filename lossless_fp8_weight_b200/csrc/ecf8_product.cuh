@@ -218,6 +218,14 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     adapter_steps = (units + 1) / 2;
   };
 
+  // P = 2, by all threads: either CTA's apart_s has what both have stored there.  (The products' barriers order the
+  // stores of the pair's even CTA for that CTA only.)
+  auto share_apart = [&] {
+    if (P != 2 || !a.rank) return;
+    __syncwarp();
+    cluster_sync();
+  };
+
   uint32_t next = 0, next_turn = 0;  // warp 0: the next stage to load, and the parity of its use
   if (warp == 0) {
     if (elect_one()) {
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (++next == a.stages) next = 0, next_turn ^= 1;
     }
     find_adapters();
+    share_apart();
   } else if (warp == 1) {
     if (side != 0) {
       find_adapters();
@@ -299,6 +308,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
       if (ok && elect_one()) mma_commit<P>(done, mask);
       __syncwarp();
     }
+    share_apart();
   } else {
     const int w4 = warp - 2, quarter = warp % 4, group = w4 / 4;
     const uint32_t row = quarter * 32 + lane;
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
     ok = ok && mbar_wait(done, 0, waits);
     if (ok) fence_after();
     wait_predecessor();  // row_id and p are there, and nothing before this call reads the output any more
-    if (P == 2) asm volatile("bar.sync 1, %0;" ::"n"(128 * G) : "memory");  // apart_s
+    share_apart();
 
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
     T* out = static_cast<T*>(a.out);

@@ -118,3 +118,21 @@ def test_a_wait_that_runs_out_is_reported(env, rows, n, k, kernel):
         limits(kernel, 0, 0)
     got, status = checked.run()
     assert status == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("at", [0, 100, 127, 128, 200, 255, 256, 300])
+def test_a_row_that_is_not_finite_in_either_half_of_a_tile(env, at):
+    """Tiles of a pair of CTAs, each of which reads half of the rows: an infinity of one row's A x is in all of its
+    columns, and in no other row.  (x and W x are finite.)"""
+    L, torch = env
+    c = Case(env, 310, 4864, 128, 16, 2, [310], [1], "bf16", 1, seed=33)
+    c.x[at, 3:5] = 3e38
+    c.a[1, :, 3:5] = 1.0
+    c.w[:, 3:5] = 0
+    y, u = c.forward()
+    assert bool(u[at].isinf().all())
+    assert not bool(y[at].isfinite().any())
+    rest = torch.arange(310, device="cuda") != at
+    assert bool(y[rest].isfinite().all())
+    want, _, size, pairs = c.exact_forward()
+    c.near(y[rest], want[rest], size[rest], 128 + 16, pairs[rest])
