@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(64 + 128 * G, P == 2 ? 1 : 2)
             }
         }
         if (!ok) break;
+        __syncwarp();
         fence_after();
         tmem_st32(widened(s) + lanes, v);
         fence_async();

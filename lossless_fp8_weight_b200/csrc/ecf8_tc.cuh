@@ -229,8 +229,10 @@ __device__ inline void tmem_st16(uint32_t tmem, const uint32_t (&v)[16]) {
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
-// The wait is part of the statement: nothing may read v between the two.
+// The wait is part of the statement: nothing may read v between the two.  The lanes have to be together, which after a
+// branch of some (the columns or rows that exist) they need not be.
 __device__ inline void tmem_ld16(uint32_t tmem, float (&v)[16]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];\n"
@@ -241,6 +243,7 @@ __device__ inline void tmem_ld16(uint32_t tmem, float (&v)[16]) {
       : "memory");
 }
 __device__ inline void tmem_ld8(uint32_t tmem, float (&v)[8]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
       "tcgen05.wait::ld.sync.aligned;"
