@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(kOuterThreads, 2)
     __syncwarp();
   }
   T* out = static_cast<T*>(side.out) + (uint64_t)id * a.rank * side.cols;
-  const float alpha = a.alpha[id] / (Widen<T>::kBf16 ? 1.0f : unit_of(side.peak[id]));
+  // an adapter without rows gets zeros, whatever its alpha
+  const float alpha = seen ? a.alpha[id] / (Widen<T>::kBf16 ? 1.0f : unit_of(side.peak[id])) : 0.0f;
   if (warp >= 2) {
     const int quarter = warp % 4, half = (warp - 2) / 4;
     const uint32_t row = quarter * 32 + lane;
@@ -711,9 +712,11 @@ __global__ void __launch_bounds__(128) outer_simple(const float* p, uint32_t ran
   const uint32_t r0 = blockIdx.y * 8, nr = min(8u, rank - r0);
   const int32_t a = (int32_t)blockIdx.z;
   float acc[8] = {};
+  bool any = false;
   for (uint32_t i = 0; i < count; ++i) {
     if (ids[i] != a) continue;
     const int64_t b = max(0, offsets[i]), e = min((int64_t)offsets[i + 1], (int64_t)rows);
+    any |= e > b;
     if (c < cols)
       for (int64_t t = b; t < e; ++t) {
         const float x = to_float(q[(uint64_t)t * q_stride + c]);
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(128) outer_simple(const float* p, uint32_t ran
   if (c < cols)
 #pragma unroll
     for (uint32_t r = 0; r < 8; ++r)
-      if (r < nr) put(out + (uint64_t)a * f_adapter + (r0 + r) * sr + c * sc, alpha[a] * acc[r]);
+      if (r < nr) put(out + (uint64_t)a * f_adapter + (r0 + r) * sr + c * sc, any ? alpha[a] * acc[r] : 0.0f);
 }
 
 #ifdef ECF8_CHECKED

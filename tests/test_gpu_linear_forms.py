@@ -136,3 +136,22 @@ def test_a_row_that_is_not_finite_in_either_half_of_a_tile(env, at):
     assert bool(y[rest].isfinite().all())
     want, _, size, pairs = c.exact_forward()
     c.near(y[rest], want[rest], size[rest], 128 + 16, pairs[rest])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,n,k,shift", [(70, 256, 512, 0), (70, 256, 512, 3), (2100, 256, 128, 0)])
+def test_adapters_without_rows_get_zeros_whatever_their_alpha(env, rows, n, k, shift, dtype):
+    """By both kinds of kernel: x and dy whose rows start off 16-byte bounds (shift) take the plain ones."""
+    L, torch = env
+    alpha = torch.tensor([float("nan"), 0.5, float("inf"), float("-inf")], device="cuda")
+    c = Case(env, rows, n, k, 16, 4, [rows, 0], [1, 2], dtype, 1, seed=34, alpha=alpha)
+    _, u = c.forward()
+    if shift:
+        c.x, c.dy = (torch.nn.functional.pad(t, (shift, 2))[:, shift:-2] for t in (c.x, c.dy))
+    _, da, db = c.backward(u)
+    for i in (0, 2, 3):
+        assert bool((da[i] == 0).all()) and bool((db[i] == 0).all())
+    _, wda, wdb, _, _, sa, sb = c.exact_backward(u)
+    c.near(da[1], wda[1], sa[1], rows + n, sa[1])
+    c.near(db[1], wdb[1], sb[1], rows, sb[1])
+    assert int(c.status.item()) == 0
