@@ -392,6 +392,12 @@ typedef struct ecf8_requests {
  * the slower kernels. */
 size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows);
 
+/* CTAs that share a tile of the projection (backward = 0) or of its input
+ * gradient when a call of this many rows takes the tensor cores: 2 in large
+ * calls, else 1; 0 for bad arguments.  For reading times, and for tests that
+ * have to reach one form or the other. */
+int ecf8_linear_tile_ctas(const ecf8_linear* lin, uint64_t rows, int backward);
+
 /* y = s * (x W^T) + the adapters' part, for `rows` rows.  requests may be NULL
  * (no row has an adapter).  d_u (nullable; float32, rows x rank) keeps A[a] x[t] for
  * a backward pass, 0 for rows without an adapter; NULL keeps it in the

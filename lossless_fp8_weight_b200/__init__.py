@@ -597,6 +597,7 @@ class RequestsDesc(ctypes.Structure):
 _u64 = ctypes.c_uint64
 _lib.ecf8_linear_workspace_size.argtypes = [ctypes.POINTER(LinearDesc), _u64]
 _lib.ecf8_linear_workspace_size.restype = _sz
+_lib.ecf8_linear_tile_ctas.argtypes = [ctypes.POINTER(LinearDesc), _u64, _i32]
 _lib.ecf8_linear_forward.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(RequestsDesc), _p, _u64, _p, _u64, _u64,
                                      _p, _p, _sz, _p, _p]
 _lib.ecf8_linear_backward.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(RequestsDesc), _p, _u64, _p, _u64, _p,
@@ -656,6 +657,10 @@ class Linear:
     def workspace_size(self, rows: int) -> int:
         """Bytes of device workspace forward and backward need for this many rows."""
         return int(_lib.ecf8_linear_workspace_size(self._ref, rows))
+
+    def tile_ctas(self, rows: int, backward: bool = False) -> int:
+        """CTAs that share a tile of the projection, or of its input gradient, in a call of this many rows."""
+        return int(_lib.ecf8_linear_tile_ctas(self._ref, rows, int(backward)))
 
     def _requests(self, q):
         if q is None:

@@ -907,6 +907,11 @@ bool tensor_path(const Operands& o, const void* q, uint64_t q_stride) {
   return o.weight && small_enough(o.l) && tma_rows(q, q_stride, 2);
 }
 
+// Two CTAs to a tile of 256 columns where such tiles occupy half of the SMs at least; else single ones, two to an SM, on
+// tiles of at most 128 rows, which give more CTAs before the reduction has to be split (256 rows of 1024x4096 backward:
+// 29 us in pairs, 16 us so; 200 rows of 4096x4096: 33 and 21).
+bool in_pairs(uint64_t rows, uint64_t cols) { return rows > 128 && (cols + 255) / 256 * ((rows + 255) / 256) >= 37; }
+
 template <class T, int BACK>
 int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t in_stride, void* out,
                    uint64_t out_stride, uint64_t rows, const int32_t* row_id, const float* p, bool overlap,
@@ -916,10 +921,7 @@ int product_tensor(const ecf8_linear* l, bool adapted, const void* in, uint64_t 
   a.rows = rows;
   a.cols = cols;
   a.len = len;
-  // Two CTAs to a tile of 256 columns where such tiles occupy half of the SMs at least; else single ones, two to an SM,
-  // on tiles of at most 128 rows, which give more CTAs before the reduction has to be split (256 rows of 1024x4096
-  // backward: 29 us in pairs, 16 us so; 200 rows of 4096x4096: 33 and 21).
-  const bool pair = rows > 128 && (cols + 255) / 256 * ((rows + 255) / 256) >= 37;
+  const bool pair = in_pairs(rows, cols);
   const uint64_t tall = pair ? 256 : 128;
   a.bt = (uint32_t)(rows >= tall ? tall : (rows + 15) / 16 * 16);
   const int kb = pair ? 1 : 2, width = pair ? 2 : 1;
@@ -1230,6 +1232,11 @@ void ecf8_checked_limits(int kernel, long long cycles, uint32_t missing) {
 
 size_t ecf8_linear_workspace_size(const ecf8_linear* lin, uint64_t rows) {
   return lin && rows < kMost ? plan_of(lin, rows).total : 0;
+}
+
+int ecf8_linear_tile_ctas(const ecf8_linear* lin, uint64_t rows, int backward) {
+  if (!lin || !rows || rows >= kMost) return 0;
+  return in_pairs(rows, backward ? lin->k_in : lin->n_out) ? 2 : 1;
 }
 
 int ecf8_linear_forward(const ecf8_linear* lin, const ecf8_requests* requests, const void* d_x, uint64_t x_stride,

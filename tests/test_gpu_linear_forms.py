@@ -155,3 +155,230 @@ def test_adapters_without_rows_get_zeros_whatever_their_alpha(env, rows, n, k, s
     c.near(da[1], wda[1], sa[1], rows + n, sa[1])
     c.near(db[1], wdb[1], sb[1], rows, sb[1])
     assert int(c.status.item()) == 0
+
+
+# ---- the form of large calls: two CTAs to a tile ----
+
+def pairs(c, backward):
+    """Fails where a size no longer takes that form."""
+    assert c.linear.tile_ctas(c.rows, backward) == 2
+
+
+BACK = [
+    # rows, n, k, rank, adapters, lengths, ids; dx has 256 columns and 256 rows a tile
+    (1300, 512, 4096, 16, 3, [700, 0, 500, 90], [2, 1, 0, -1]),
+    (150, 264, 9472, 24, 2, [70, 80], [1, 0]),
+    (700, 333, 3335, 12, 5, [100, 250, 0, 300], [4, 0, 1, 4]),
+    (257, 64, 5120, 128, 2, [256], [1]),
+    (1030, 2064, 2100, 64, 9, [100] * 10, [8, 7, 6, 5, 4, 3, 2, 1, 0, 8]),
+    (600, 72, 3328, 1, 1, [600], [0]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_scale", [0, 1, "row"])
+@pytest.mark.parametrize("size", BACK, ids=lambda s: "x".join(map(str, s[:4])))
+def test_large_input_gradients_equal_the_formula(env, size, n_scale, dtype):
+    c = Case(env, *size, dtype, n_scale, seed=size[0])
+    pairs(c, True)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n_scale", [0, 1, "row"])
+@pytest.mark.parametrize("size", BACK, ids=lambda s: "x".join(map(str, s[:4])))
+def test_large_projections_equal_the_formula(env, size, n_scale, dtype):
+    rows, n, k, *rest = size
+    c = Case(env, rows, k, n, *rest, dtype, n_scale, seed=size[0] + 1)
+    pairs(c, False)
+    c.check(backward=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_large_calls_without_adapters(env, backward, dtype):
+    L, torch = env
+    for n_scale in (0, 1, "row"):
+        n, k = (520, 4864) if backward else (4864, 520)
+        c = Case(env, 300, n, k, 1, 0, [300], [-1], dtype, n_scale, seed=41)
+        pairs(c, backward)
+        c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_one_requests_infinities_and_nans_stay_in_its_rows_of_large_calls(env, backward, dtype):
+    L, torch = env
+    rows, rank = 500, 32
+    n, k = (144, 4864) if backward else (4864, 144)
+    lengths, ids = [100, 60, 140, 40, 150], [0, 1, -1, 2, 1]
+
+    def case():
+        c = Case(env, rows, n, k, rank, 3, lengths, ids, dtype, "row", seed=42)
+        pairs(c, backward)
+        return c
+
+    c = case()
+    y0, u0 = c.forward()
+    dx0, da0, db0 = c.backward(u0)
+    bad = torch.from_numpy(c.row_ids() == 1).cuda()
+    # an adapter
+    c.a[1, 0, 3], c.b[1, 5, 0], c.b[1, 6, rank - 1], c.alpha[1] = float("inf"), float("nan"), float("-inf"), 2.0
+    y, u = c.forward()
+    dx, _, _ = c.backward(u0)
+    assert torch.equal(y[~bad], y0[~bad]) and torch.equal(u[~bad], u0[~bad])
+    assert torch.equal(dx[~bad], dx0[~bad])
+    assert torch.equal(y[bad].isnan(), c.exact_forward()[0][bad].isnan()) and bool(y[bad].isnan().any())
+    assert torch.equal(dx[bad].isnan(), c.exact_backward(u0)[0][bad].isnan()) and bool(dx[bad].isnan().any())
+    # its alpha
+    c = case()
+    c.alpha[1] = float("nan")
+    y, u = c.forward()
+    dx, da, db = c.backward(u)
+    assert torch.equal(y[~bad], y0[~bad]) and bool(y[bad].isnan().all())
+    assert torch.equal(dx[~bad], dx0[~bad]) and bool(dx[bad].isnan().all())
+    # rows of x and of dy spoil themselves, and their adapter's gradients
+    c = case()
+    c.x[100, 0], c.x[255, 1], c.dy[256, 1], c.dy[400, 2] = float("nan"), float("inf"), float("nan"), float("-inf")
+    y, u = c.forward()
+    dx, da, db = c.backward(u)
+    hit = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    hit[100] = hit[255] = True
+    assert torch.equal(y[~hit], y0[~hit]) and bool(y[100].isnan().all()) and not bool(y[255].isfinite().any())
+    hit = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    hit[256] = hit[400] = True
+    assert torch.equal(dx[~hit], dx0[~hit]) and bool(dx[256].isnan().all()) and not bool(dx[400].isfinite().any())
+    for i in (0, 2):
+        assert torch.equal(da[i], da0[i]) and torch.equal(db[i], db0[i])
+    assert bool(da[1].isnan().any()) and bool(db[1].isnan().any())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 1e30, -0.5, float("inf")])
+def test_rows_of_unusual_scale_in_large_calls(env, scale, dtype):
+    L, torch = env
+    c = Case(env, 300, 4864, 264, 16, 2, [130, 170], [1, 0], dtype, "row", seed=43)
+    pairs(c, False)
+    c.scale[5], c.scale[4863] = scale, -scale
+    c.make()
+    y, _ = c.forward()
+    want, _, size, pair = c.exact_forward()
+    keep = torch.ones(4864, dtype=torch.bool, device="cuda")
+    if scale > 1:
+        for i in (5, 4863):
+            keep[i] = False
+            if dtype == "fp16" or scale == float("inf"):
+                assert torch.equal(y[:, i], want[:, i].to(c.dtype))  # infinities
+    c.near(y[:, keep], want[:, keep], size[:, keep], 264 + 16, pair[:, keep])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,n,k", [(300, 264, 4864), (60, 264, 512)])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, -0.5, float("inf")])
+def test_rows_of_unusual_scale_in_input_gradients(env, scale, rows, n, k, dtype):
+    L, torch = env
+    c = Case(env, rows, n, k, 16, 2, [rows - 20, 20], [1, 0], dtype, "row", seed=44)
+    if rows == 300:
+        pairs(c, True)
+    c.scale[5] = scale
+    c.make()
+    u = c.forward()[1]
+    dx, _, _ = c.backward(u)
+    want, _, _, size, pair, _, _ = c.exact_backward(u)
+    if scale == float("inf"):
+        assert torch.equal(dx.isnan(), want.isnan())
+        assert torch.equal(dx.double()[~want.isnan()], want[~want.isnan()]) and not bool(dx.isfinite().any())
+    else:
+        c.near(dx, want, size, n + 16, pair)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_nan_weights_reach_the_outputs_of_large_calls_that_read_them(env, backward):
+    L, torch = env
+    n, k = (144, 4864) if backward else (4864, 144)
+    for n_scale in (1, "row"):
+        c = Case(env, 300, n, k, 8, 1, [300], [0], "bf16", n_scale, seed=45)
+        pairs(c, backward)
+        c.w[3, 7], c.w[n - 1, k - 1] = 0x7F, 0xFF
+        y, u = c.forward()
+        dx, _, _ = c.backward(u)
+        for got, size, at in ((y, n, (3, n - 1)), (dx, k, (7, k - 1))):
+            nan = torch.zeros(size, dtype=torch.bool, device="cuda")
+            nan[list(at)] = True
+            assert torch.equal(got.isnan(), nan.expand(300, size))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("backward", [False, True])
+def test_large_calls_repeated_captured_and_on_another_stream(env, backward, dtype):
+    L, torch = env
+    n, k = (272, 4864) if backward else (4864, 272)
+    c = Case(env, 400, n, k, 40, 3, [130, 0, 200, 1], [1, 2, 0, 1], dtype, "row", seed=46)
+    pairs(c, backward)
+    y, u = c.forward()
+    grads = c.backward(u)
+    first = [t.clone() for t in (y, u, *grads)]
+
+    def same(now):
+        assert all(torch.equal(a, b) for a, b in zip(now, first))
+
+    for _ in range(5):
+        c.ws.random_(0, 256)
+        y2, u2 = c.forward()
+        same([y2, u2, *c.backward(u2)])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        y2, u2 = c.forward()
+        grads2 = c.backward(u2)
+    side.synchronize()
+    same([y2, u2, *grads2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.linear.forward(c.x, y, requests=c.requests, u=u, workspace=c.ws, status=c.status)
+        c.linear.backward(c.x, c.dy, u, dx=grads[0], da=grads[1], db=grads[2], requests=c.requests, workspace=c.ws,
+                          status=c.status)
+    for t in (y, u, *grads):
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    same([y, u, *grads])
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_bad_request_tables_in_large_calls(env, backward):
+    L, torch = env
+    n, k = (272, 4864) if backward else (4864, 272)
+    rows = 300
+    c = Case(env, rows, n, k, 16, 2, [rows], [1], "bf16", 1, seed=47)
+    pairs(c, backward)
+    for offsets, ids in (([0, rows + 1], [0]), ([0, 10, 5, rows], [0, 1, 1]), ([-3, 5], [1]), ([0, 5], [2]),
+                         ([0, 2 ** 31 - 1], [0]), ([5, -2 ** 31], [0])):
+        c.requests = L.Requests(torch.tensor(offsets, dtype=torch.int32, device="cuda"),
+                                torch.tensor(ids, dtype=torch.int32, device="cuda"))
+        c.status.zero_()
+        y, u = c.forward()
+        assert int(c.status.item()) == L.STATUS_BAD_REQUEST
+        c.status.zero_()
+        c.backward(u)
+        assert int(c.status.item()) == L.STATUS_BAD_REQUEST
+
+
+def test_large_calls_write_nothing_past_their_outputs(env):
+    L, torch = env
+    for rows, n, k, rank in ((261, 4880, 4936, 24), (300, 4871, 4867, 7)):
+        c = Case(env, rows, n, k, rank, 2, [rows - 1], [1], "bf16", "row", seed=48)
+        pairs(c, False)
+        pairs(c, True)
+        flats = [torch.full((rows * m + 4096,), 5.0, dtype=c.dtype, device="cuda") for m in (n, k)]
+        y, dx = (f[2048:2048 + rows * m].view(rows, m) for f, m in zip(flats, (n, k)))
+        u = torch.zeros(rows, rank, device="cuda")
+        c.linear.forward(c.x, y, requests=c.requests, u=u, workspace=c.ws)
+        c.linear.backward(None, c.dy, None, dx=dx, requests=c.requests, workspace=c.ws)
+        torch.cuda.synchronize()
+        for f in flats:
+            assert bool((f[:2048] == 5).all()) and bool((f[-2048:] == 5).all())
+        want, _, size, pair = c.exact_forward()
+        c.near(y, want, size, k + rank, pair)
