@@ -229,9 +229,10 @@ def histogram_device(d_fp8, stream=None) -> np.ndarray:
     call waits for it and returns a host array)."""
     import torch
     n = d_fp8.numel()
-    d_hist = torch.empty(16, dtype=torch.int64, device=d_fp8.device)
-    _check(_lib.ecf8_histogram_device(_ptr(d_fp8), n, _ptr(d_hist), _stream(stream)), "ecf8_histogram_device")
-    return d_hist.cpu().numpy().astype(np.uint64)
+    with torch.cuda.stream(_torch_stream(stream, d_fp8.device)):  # the copy waits for the stream it is made on
+        d_hist = torch.empty(16, dtype=torch.int64, device=d_fp8.device)
+        _check(_lib.ecf8_histogram_device(_ptr(d_fp8), n, _ptr(d_hist), _stream(stream)), "ecf8_histogram_device")
+        return d_hist.cpu().numpy().astype(np.uint64)
 
 
 def encode_device(d_fp8, codebook: Optional[Codebook] = None, chunk_bytes: int = DEFAULT_CHUNK_BYTES,
@@ -308,6 +309,14 @@ def _stream(stream) -> int:
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
+
+
+def _torch_stream(stream, device):
+    """The same as a torch stream, for what torch allocates and copies on the library's behalf."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.current_stream(device) if stream is None else torch.cuda.ExternalStream(_stream(stream), device)
 
 
 def decode(info: Info, d_blob, d_out, status=None, stream=None, blob_size: Optional[int] = None) -> None:
