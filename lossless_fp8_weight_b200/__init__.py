@@ -238,9 +238,11 @@ def histogram_device(d_fp8, stream=None) -> np.ndarray:
 def encode_device(d_fp8, codebook: Optional[Codebook] = None, chunk_bytes: int = DEFAULT_CHUNK_BYTES,
                   group_chunks: int = DEFAULT_GROUP_CHUNKS, max_len: int = 16, stream=None, hist=None):
     """Compress a CUDA uint8 tensor of E4M3 bytes on the GPU; returns the blob
-    as a CUDA uint8 tensor (the same bytes as ``encode`` of the same input)."""
+    as a CUDA uint8 tensor (the same bytes as ``encode`` of the same input).
+    On a stream given by its number the blob has to live until it is written."""
     import torch
-    x = d_fp8.reshape(-1)
+    with torch.cuda.stream(_torch_stream(stream, d_fp8.device)):  # where a tensor with gaps is copied
+        x = d_fp8.reshape(-1)
     if x.dtype != torch.uint8:
         x = x.view(torch.uint8)
     n = x.numel()
@@ -250,7 +252,10 @@ def encode_device(d_fp8, codebook: Optional[Codebook] = None, chunk_bytes: int =
     _check(_lib.ecf8_encoded_size(h.ctypes.data, n, ctypes.byref(cb), chunk_bytes, group_chunks, ctypes.byref(size)),
            "ecf8_encoded_size")
     blob = torch.empty(size.value, dtype=torch.uint8, device=x.device)
-    ws = torch.empty(max(16, _lib.ecf8_encode_device_workspace_size(n)), dtype=torch.uint8, device=x.device)
+    if isinstance(stream, torch.cuda.Stream):
+        blob.record_stream(stream)
+    with torch.cuda.stream(_torch_stream(stream, x.device)):  # the stream's own memory, reused after the call on it
+        ws = torch.empty(max(16, _lib.ecf8_encode_device_workspace_size(n)), dtype=torch.uint8, device=x.device)
     got = ctypes.c_size_t(0)
     _check(_lib.ecf8_encode_device(_ptr(x), n, h.ctypes.data, ctypes.byref(cb), chunk_bytes, group_chunks, _ptr(blob),
                                    blob.numel(), ctypes.byref(got), _ptr(ws), ws.numel(), _stream(stream)),

@@ -34,3 +34,22 @@ def test_a_histogram_waits_for_its_own_stream(env, raw):
             torch.cuda._sleep(BUSY)
         h = L.histogram_device(d, stream=_as(side, raw))
         assert np.array_equal(h, np.bincount((x >> 3) & 15, minlength=16).astype(np.uint64))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_an_encoders_workspace_outlives_the_call(env, raw):
+    """Memory that the current stream gets right after the call is none that the encoder still has to use."""
+    L, torch = env
+    x = synth.single_normal_1k().tensors[0].generate(count=3_000_001)
+    want = oracle.encode(x)
+    d, side = torch.from_numpy(np.stack([x, x], axis=1)).cuda()[:, 0], torch.cuda.Stream()  # with gaps: it is copied
+    h = L.histogram(x)
+    size = L._lib.ecf8_encode_device_workspace_size(x.size)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    blob = L.encode_device(d, hist=h, stream=_as(side, raw))
+    junk = [torch.full((m,), 0xFF, dtype=torch.uint8, device="cuda") for m in (size, size, x.size, x.size)]
+    torch.cuda.synchronize()
+    assert np.array_equal(blob.cpu().numpy(), want)
+    assert all(bool((j == 0xFF).all()) for j in junk)
