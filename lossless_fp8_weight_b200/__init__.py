@@ -230,6 +230,7 @@ def histogram_device(d_fp8, stream=None) -> np.ndarray:
     import torch
     n = d_fp8.numel()
     with torch.cuda.stream(_torch_stream(stream, d_fp8.device)):  # the copy waits for the stream it is made on
+        d_fp8 = d_fp8.contiguous()
         d_hist = torch.empty(16, dtype=torch.int64, device=d_fp8.device)
         _check(_lib.ecf8_histogram_device(_ptr(d_fp8), n, _ptr(d_hist), _stream(stream)), "ecf8_histogram_device")
         return d_hist.cpu().numpy().astype(np.uint64)
@@ -242,7 +243,7 @@ def encode_device(d_fp8, codebook: Optional[Codebook] = None, chunk_bytes: int =
     On a stream given by its number the blob has to live until it is written."""
     import torch
     with torch.cuda.stream(_torch_stream(stream, d_fp8.device)):  # where a tensor with gaps is copied
-        x = d_fp8.reshape(-1)
+        x = d_fp8.contiguous().reshape(-1)
     if x.dtype != torch.uint8:
         x = x.view(torch.uint8)
     n = x.numel()

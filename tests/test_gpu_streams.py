@@ -36,6 +36,14 @@ def test_a_histogram_waits_for_its_own_stream(env, raw):
         assert np.array_equal(h, np.bincount((x >> 3) & 15, minlength=16).astype(np.uint64))
 
 
+def test_a_vector_with_gaps_is_counted_and_encoded_by_its_values(env):
+    L, torch = env
+    x = synth.single_normal_1k().tensors[0].generate(count=70_001)
+    d = torch.from_numpy(np.stack([x, np.zeros_like(x)], axis=1)).cuda()[:, 0]
+    assert np.array_equal(L.histogram_device(d), np.bincount((x >> 3) & 15, minlength=16).astype(np.uint64))
+    assert np.array_equal(L.encode_device(d).cpu().numpy(), oracle.encode(x))
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_an_encoders_workspace_outlives_the_call(env, raw):
     """Memory that the current stream gets right after the call is none that the encoder still has to use."""
