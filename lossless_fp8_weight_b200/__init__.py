@@ -750,7 +750,9 @@ class GradSet:
     types) receives the clipped values; by default they are written in place.
     The descriptor table is laid out and copied to the device here, once; the
     set's tensors must stay where they are.  Calls that can overlap on the GPU
-    need sets of their own."""
+    need sets of their own.  A set may be dropped once its calls are made; on a
+    stream given by its number, or captured into a graph, it has to live as
+    long as they can run."""
 
     def __init__(self, grads, outs=None):
         import torch
@@ -773,6 +775,17 @@ class GradSet:
         self._keep = (grads, outs)
         self._args = (self._h.ctypes.data, _ptr(self._d))
         self._ws_args = (_ptr(self._ws), self._ws.numel())
+        self._streams = {_stream(None)}  # those that the table's and the workspace's memory is known to serve
+
+    def _on(self, stream) -> int:
+        """The stream's number; the set's memory is not given to another use before the stream is done with it."""
+        number = _stream(stream)
+        if number not in self._streams and not isinstance(stream, int):
+            stream = _torch_stream(stream, self._device)
+            self._d.record_stream(stream)
+            self._ws.record_stream(stream)
+            self._streams.add(number)
+        return number
 
     def _one(self, norm, status) -> None:
         if str(norm.dtype) != "torch.float32" or norm.numel() != 1:
@@ -782,12 +795,12 @@ class GradSet:
     def norm(self, norm, status=None, stream=None) -> None:
         """Asynchronously writes the L2 norm of the whole set to ``norm`` (one float32)."""
         self._one(norm, status)
-        _check(_lib.ecf8_grad_norm(*self._args, _ptr(norm), *self._ws_args, _ptr(status), _stream(stream)),
-               "ecf8_grad_norm")
+        _check(_lib.ecf8_grad_norm(*self._args, _ptr(norm), *self._ws_args, _ptr(status),
+                                   self._on(stream)), "ecf8_grad_norm")
 
     def clip(self, max_norm: float, norm, status=None, stream=None) -> None:
         """``norm``, then every tensor times min(1, max_norm / (norm + 1e-6)).
         A norm that is not finite sets ECF8_STATUS_NONFINITE and changes no value."""
         self._one(norm, status)
         _check(_lib.ecf8_grad_clip(*self._args, float(max_norm), _ptr(norm), *self._ws_args, _ptr(status),
-                                   _stream(stream)), "ecf8_grad_clip")
+                                   self._on(stream)), "ecf8_grad_clip")

@@ -61,3 +61,32 @@ def test_an_encoders_workspace_outlives_the_call(env, raw):
     torch.cuda.synchronize()
     assert np.array_equal(blob.cpu().numpy(), want)
     assert all(bool((j == 0xFF).all()) for j in junk)
+
+
+@pytest.mark.parametrize("how", ["stream", "current", "norm"])
+def test_a_gradient_set_may_be_dropped_before_its_call_runs(env, how):
+    """Its table and workspace are no memory that the stream it was made on hands out meanwhile."""
+    L, torch = env
+    grads = [torch.randn(1000 + i, device="cuda") for i in range(300)]
+    want = float(torch.stack([g.double().square().sum() for g in grads]).sum().sqrt())
+    before = [g.clone() for g in grads]
+    norm, side = torch.zeros(1, device="cuda"), torch.cuda.Stream()
+    L.GradSet(before, [torch.empty_like(b) for b in before]).clip(1.0, norm)  # the first launch loads the kernels
+    s = L.GradSet(grads)
+    torch.cuda.synchronize()
+    own = {t.data_ptr(): t.numel() for t in (s._d, s._ws)}
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        if how == "current":
+            s.clip(1.0, norm)
+    if how == "stream":
+        s.clip(1.0, norm, stream=side)
+    elif how == "norm":
+        s.norm(norm, stream=side)
+    del s
+    junk = [torch.full((m,), 0, dtype=torch.uint8, device="cuda") for _ in range(4) for m in own.values()]
+    assert not own.keys() & {j.data_ptr() for j in junk}
+    torch.cuda.synchronize()
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want
+    factor = 1.0 if how == "norm" else 1.0 / (want + 1e-6)
+    assert all(bool(((g - b * factor).abs() <= 2.0 ** -21 * b.abs()).all()) for g, b in zip(grads, before))
