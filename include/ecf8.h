@@ -461,7 +461,7 @@ int ecf8_grad_norm(const void* h_table, const void* d_table, float* d_norm, void
 
 /* ecf8_grad_norm, then out = in * min(1, max_norm / (norm + 1e-6)) for every
  * tensor (max_norm >= 0; the product in float32, rounded once).  A norm that
- * is not finite ORs ECF8_STATUS_NONFINITE into *d_status and the factor is 1:
+ * is not finite as float32 ORs ECF8_STATUS_NONFINITE into *d_status and the factor is 1:
  * the gradients stay as they are, for the caller to skip the step.  Every
  * tensor needs a d_out (ECF8_ERR_ARG). */
 int ecf8_grad_clip(const void* h_table, const void* d_table, float max_norm, float* d_norm, void* d_workspace,

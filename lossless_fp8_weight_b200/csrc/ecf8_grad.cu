@@ -12,7 +12,7 @@
 // A tensor is cut into chunks of kChunk values; each CTA takes a contiguous run
 // of the set's chunks, finds its first tensor by a binary search and walks on
 // from there.  Squares are summed in float64 (a float32 squared is exact in it,
-// and no norm that is finite overflows), per thread, then per CTA in a fixed
+// and no sum of them overflows), per thread, then per CTA in a fixed
 // tree, then over the CTAs' sums in index order, so the result does not vary.
 // Conversions to float64 run at a quarter of the rate of other instructions,
 // which for 16-bit values is less than memory delivers: four of those are
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) clip_kernel(const Header* table, uin
   for (uint32_t i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
   const double norm = sqrt(block_sum(s));
   const float shown = (float)norm;
-  const bool finite = isfinite(norm);
+  const bool finite = isfinite(shown);  // as the caller sees it
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *d_norm = shown;
     if (!finite && d_status) atomicOr(d_status, ECF8_STATUS_NONFINITE);
