@@ -748,6 +748,8 @@ class GradSet:
     mixed as they come) whose global L2 norm is taken, and which are clipped by
     it, in one call (ecf8_grad_* in the C ABI).  ``outs`` (same sizes and
     types) receives the clipped values; by default they are written in place.
+    None in the place of an output: only the norm is wanted, and tensors may
+    share memory.
     The descriptor table is laid out and copied to the device here, once; the
     set's tensors must stay where they are.  Calls that can overlap on the GPU
     need sets of their own.  A set may be dropped once its calls are made; on a
@@ -762,7 +764,8 @@ class GradSet:
             _refuse("GradSet", f"{len(grads)} tensors, {len(outs)} outputs")
         arr = (Grad * max(1, len(grads)))()
         for i, (g, o) in enumerate(zip(grads, outs)):
-            if not g.is_contiguous() or not o.is_contiguous() or o.dtype != g.dtype or o.numel() != g.numel():
+            if not g.is_contiguous() or (o is not None and (not o.is_contiguous() or o.dtype != g.dtype
+                                                            or o.numel() != g.numel())):
                 _refuse("GradSet", f"tensor {i}: want contiguous tensors, the output of the same type and size")
             arr[i] = Grad(_ptr(g), _ptr(o), g.numel(), _dtype_of(g, f"GradSet tensor {i}"))
         self._h = np.zeros(int(_lib.ecf8_grad_table_bytes(len(grads))), dtype=np.uint8)

@@ -33,3 +33,23 @@ def test_the_status_tells_what_the_norm_shows(env, values, finite, in_place):
             assert bool(((g.double() - exact).abs() <= most).all())
         else:
             assert torch.equal(g, b)
+
+
+def test_sets_of_which_only_the_norm_is_wanted(env):
+    """Without outputs a tensor may be listed twice, or lie in another; such a set is not clipped."""
+    L, torch = env
+    g = torch.randn(5000, device="cuda")
+    grads = [g, g[100:700], g, g[3:4], g.to(torch.bfloat16)]
+    before, norm = g.clone(), torch.zeros(1, device="cuda")
+    s = L.GradSet(grads, [None] * 5)
+    s.norm(norm)
+    want = float(sum((t.double() ** 2).sum() for t in grads).sqrt())
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want and torch.equal(g, before)
+    with pytest.raises(L.Ecf8Error) as e:
+        s.clip(1.0, norm)
+    assert e.value.code == -1
+    # one output missing is one too few
+    with pytest.raises(L.Ecf8Error):
+        L.GradSet([g, g.clone()], [torch.empty_like(g), None]).clip(1.0, norm)
+    torch.cuda.synchronize()
+    assert torch.equal(g, before)
