@@ -623,7 +623,7 @@ class Linear:
     """y = scale * (x W^T) over decoded E4M3 weights, with the low-rank
     adapters of many requests added (ecf8_linear_* in the C ABI).
 
-    ``weight`` is a CUDA uint8 tensor (out, in) with contiguous rows, or the
+    ``weight`` is a CUDA uint8 or float8_e4m3fn tensor (out, in) with contiguous rows, or the
     address at which a decode writes it (as ``Pipeline.acquire`` returns, plus
     the tensor's offset) with ``shape`` given.  ``scale``: float32 CUDA tensor
     of 1 or ``out`` values, or None.  ``dtype``: torch.bfloat16 or
@@ -645,7 +645,7 @@ class Linear:
             if weight.dim() != 2 or (shape is not None and tuple(shape) != tuple(weight.shape)):
                 _refuse("Linear", f"want a weight of 2 dimensions, got {tuple(weight.shape)}")
             n, k = weight.shape
-            if weight.element_size() != 1:
+            if weight.dtype not in (torch.uint8, torch.float8_e4m3fn):  # other bytes mean other values
                 _refuse("Linear", f"weights are E4M3 bytes, got {weight.dtype}")
             d.w_stride = _rows(weight, "Linear weight", weight.dtype, n, k)
         d.d_w, d.n_out, d.k_in, d.dtype = _ptr(weight), n, k, _DTYPES[str(dtype)]
