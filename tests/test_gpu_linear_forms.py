@@ -382,3 +382,62 @@ def test_large_calls_write_nothing_past_their_outputs(env):
             assert bool((f[:2048] == 5).all()) and bool((f[-2048:] == 5).all())
         want, _, size, pair = c.exact_forward()
         c.near(y, want, size, k + rank, pair)
+
+
+# ---- calls at the edges of what the entry points take ----
+
+def test_no_rows_no_requests_no_table(env):
+    """No rows: adapters' gradients are zeros.  No table: no row has an adapter."""
+    L, torch = env
+    c = Case(env, 40, 256, 512, 16, 2, [40], [1], "bf16", "row", seed=51)
+    da, db = torch.full_like(c.a, 7.0), torch.full_like(c.b, 7.0)
+    u0 = torch.empty(0, 16, device="cuda")
+    c.linear.forward(c.x[:0], torch.empty(0, 256, dtype=c.dtype, device="cuda"), requests=c.requests, u=u0,
+                     workspace=c.ws, status=c.status)
+    c.linear.backward(c.x[:0], c.dy[:0], u0, dx=torch.empty_like(c.x[:0]), da=da, db=db, requests=c.requests,
+                      workspace=c.ws, status=c.status)
+    assert not bool(da.any()) and not bool(db.any())
+    plain = L.Linear(c.w, scale=c.scale, dtype=c.dtype)
+    y, want = torch.empty_like(c.dy), torch.empty_like(c.dy)
+    dx, wdx = torch.empty_like(c.x), torch.empty_like(c.x)
+    u = torch.full((40, 16), 9.0, device="cuda")
+    c.linear.forward(c.x, y, u=u, workspace=c.ws, status=c.status)
+    plain.forward(c.x, want)
+    assert torch.equal(y, want) and not bool(u.any())
+    da.fill_(7.0), db.fill_(7.0)
+    c.linear.backward(c.x, c.dy, u, dx=dx, da=da, db=db, workspace=c.ws, status=c.status)
+    plain.backward(None, c.dy, None, dx=wdx)
+    assert torch.equal(dx, wdx) and not bool(da.any()) and not bool(db.any())
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("rows,n,k", [(700, 96, 160), (700, 4864, 96), (700, 96, 4864)])
+@pytest.mark.parametrize("adapters,rank", [(700, 3), (300, 16), (65535, 1)])
+def test_many_adapters(env, rows, n, k, adapters, rank):
+    """A row each of its own adapter, the last one's among them."""
+    L, torch = env
+    ids = [(adapters - 1 - 7 * i) % adapters for i in range(rows)]
+    c = Case(env, rows, n, k, rank, adapters, [1] * rows, ids, "fp16", 1, seed=52)
+    y, u = c.forward()
+    dx, da, db = c.backward(u)
+    # by rows: the reference's loop over requests would take seconds
+    w, s = c.wide()
+    x, dy, at = c.x.double(), c.dy.double(), torch.tensor(ids, device="cuda")
+    a, b, al = c.a.double()[at], c.b.double()[at], c.alpha.double()[at, None]
+    wu = torch.einsum("tk,trk->tr", x, a)
+    want = (x @ w.T) * s + al * torch.einsum("tr,tnr->tn", wu, b)
+    pair = al * torch.einsum("tr,tnr->tn", torch.einsum("tk,trk->tr", x.abs(), a.abs()), b.abs())
+    c.near(y, want, (x.abs() @ w.abs().T) * s + pair, k + rank, pair)
+    v = al * torch.einsum("tn,tnr->tr", dy, b)
+    pair = al * torch.einsum("tr,trk->tk", torch.einsum("tn,tnr->tr", dy.abs(), b.abs()), a.abs())
+    c.near(dx, (dy * s) @ w + torch.einsum("tr,trk->tk", v, a), (dy.abs() * s) @ w.abs() + pair, n + rank, pair)
+    wda, wdb = torch.zeros_like(c.a, dtype=torch.float64), torch.zeros_like(c.b, dtype=torch.float64)
+    wda.index_add_(0, at, torch.einsum("tr,tk->trk", v, x))
+    wdb.index_add_(0, at, al[:, :, None] * torch.einsum("tn,tr->tnr", dy, u.double()))
+    sa, sb = torch.zeros_like(wda), torch.zeros_like(wdb)
+    va = al * torch.einsum("tn,tnr->tr", dy.abs(), b.abs())
+    sa.index_add_(0, at, torch.einsum("tr,tk->trk", va, x.abs()))
+    sb.index_add_(0, at, al[:, :, None] * torch.einsum("tn,tr->tnr", dy.abs(), u.double().abs()))
+    c.near(da, wda, sa, rows + n, sa)
+    c.near(db, wdb, sb, rows, sb)
+    assert int(c.status.item()) == 0
