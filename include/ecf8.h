@@ -358,7 +358,8 @@ void ecf8_pipeline_destroy(ecf8_pipeline* p);
  *
  * A request table that is not monotone in [0, rows] or names an adapter past
  * the last ORs ECF8_STATUS_BAD_REQUEST into *d_status; the rows it concerns
- * then get unspecified values, and nothing is accessed out of bounds. */
+ * then get unspecified values, the same in every call, and nothing is accessed
+ * out of bounds.  Without adapters (n_adapters = 0) the table is not read. */
 #define ECF8_DTYPE_BF16 0
 #define ECF8_DTYPE_FP16 1
 #define ECF8_DTYPE_FP32 2 /* gradient sets only */

@@ -152,8 +152,8 @@ __global__ void __launch_bounds__(256) product_simple(const T* q, uint64_t q_str
 // The kernel also finds the adapter of every row, for itself and for the
 // projection, which starts beside it.
 //
-// Measured: 8192 rows of 8192 at rank 64 36 us, 3.7 TB/s, 57% of the copy rate;
-// 32 rows of 4096, 24 adapters of rank 16: 12 us, the latency of its parts.
+// Measured: 8192 rows of 8192 at rank 64 37 us, 3.6 TB/s, 55% of the copy rate;
+// 32 rows of 4096, 24 adapters of rank 16: 13 us, the latency of its parts.
 
 struct ShrinkArgs {
   uint64_t rows;
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(256) transpose_kernel(const T* in, T* out, uin
 // infinities.  Few columns split the blocks over a cluster.  A CTA uses half of
 // an SM's shared and tensor memory, so that two hide each other's ends.
 //
-// Measured: both gradients at 8192 rows of 8192x8192, rank 64: 59 us, 4.6 TB/s,
-// 70% of the copy rate; the parts before it 9 us, and their peaks (FP16) 15 us.
+// Measured: both gradients at 8192 rows of 8192x8192, rank 64: 66 us, 4.1 TB/s,
+// 62% of the copy rate; the parts before it 10 us, and their peaks (FP16) 17 us.
 
 struct OuterSide {
   uint64_t cols;
@@ -907,9 +907,9 @@ bool tensor_path(const Operands& o, const void* q, uint64_t q_stride) {
   return o.weight && small_enough(o.l) && tma_rows(q, q_stride, 2);
 }
 
-// Two CTAs to a tile of 256 columns where such tiles occupy half of the SMs at least; else single ones, two to an SM, on
-// tiles of at most 128 rows, which give more CTAs before the reduction has to be split (256 rows of 1024x4096 backward:
-// 29 us in pairs, 16 us so; 200 rows of 4096x4096: 33 and 21).
+// Two CTAs to a tile of 256 columns where such tiles occupy half of the 148 SMs at least; else single ones, two to an
+// SM, on tiles of at most 128 rows, which give more CTAs before the reduction has to be split (256 rows of 1024x4096
+// backward: 29 us in pairs, 16 us so; 200 rows of 4096x4096: 33 and 21).
 bool in_pairs(uint64_t rows, uint64_t cols) { return rows > 128 && (cols + 255) / 256 * ((rows + 255) / 256) >= 37; }
 
 template <class T, int BACK>

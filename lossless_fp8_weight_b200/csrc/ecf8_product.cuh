@@ -18,13 +18,17 @@
 // its own weights and half of q (one CTA on 128 x 256 asked 12 TB/s of L2 and
 // stopped there).
 //
-// Measured without adapters.  16 rows of 28672x8192: 54 us, 4.4 TB/s, 67% of
-// the copy rate; of 8192x28672: 50 us, 72%.  8192 rows of 14336x4096: FP16
-// 0.85 ms, 1.13 PFLOP/s, 69%, BF16 0.95 ms; the input gradient at 8192 rows of
-// 8192x8192: 1.19 ms, 0.92 PFLOP/s, 56%.  What bounds it now: forward, the
-// widening warps' issue and the hand-over from load to widening to product
-// (with the widening left out it runs 15% faster); backward, the byte loads
-// that turn a column of W into a row; small calls, start and end of the CTAs.
+// Measured without adapters, FP16 and BF16, on a GPU that was idle before.  16
+// rows of 28672x8192: 52 and 58 us, 4.6 and 4.1 TB/s, 69 and 62% of the copy
+// rate; of 8192x28672: 48 and 53 us.  8192 rows of 14336x4096: 0.82 and 0.84
+// ms, 1.17 and 1.14 PFLOP/s, 71 and 69%; the input gradient at 8192 rows of
+// 8192x8192: 1.01 and 1.03 ms, 66%; at 4096 rows of 4096x4096 0.152 and 0.158
+// ms, 55%.  What bounds it now: the hand-over from load to widening to product
+// (forward the matrix unit is active for 59% of the clocks, the warps issue in
+// 34%, memory and L2 are below 30%; with the widening left out it ran 15%
+// faster), in the input gradient with the byte loads in it that turn a column
+// of W into a row (53% and 38%, the shared-memory pipe 28%); in small calls,
+// start and end of the CTAs.
 //
 // The adapters' part of large calls is more terms of the same sum,
 //     D[c][t] += sum over the tile's adapters a, ranks r of (f[a][c][r] alpha[a] / s[c]) * [a is t's] p[t][r],
@@ -38,7 +42,9 @@
 // 16-bit type holds: it enters as a 16-bit value and a 16-bit rest, two
 // products a step (one of them alone made the error up to 1.3 times that of
 // the final rounding).  2^-17 of a term is lost in BF16; in FP16 2^-23, or 2^-31
-// of the largest scale's where that is more.
+// of the largest scale's where that is more.  8192 rows of 8192x8192: 1.58 and
+// 1.56 ms, the matrix unit active for 78% of the clocks at the rate that the
+// power cap leaves it (one scale for all, one product: 1.01 and 1.03 ms).
 #ifndef ECF8_PRODUCT_CUH_
 #define ECF8_PRODUCT_CUH_
 
